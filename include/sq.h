@@ -224,6 +224,167 @@ int sq_decode_step_kda(sq_pool *pool, const int32_t *slot_ids, int32_t n_req, co
                        const void *k, const void *v, int32_t qkv_dtype, const float *alpha,
                        const float *beta, float *o, void *stream);
 
+/* The decode step without the delta correction, for recurrent layers that only
+ * decay and write:
+ *     S' = alpha S^ + beta k v^T,   o = S'^T q,   tile = encode(S')
+ * Arguments, errors and formats as for sq_decode_step (alpha and beta fp32
+ * [n_req][n_heads]).  n_req == 0 is a no-op.  Asynchronous on `stream`. */
+int sq_decode_step_linear(sq_pool *pool, const int32_t *slot_ids, int32_t n_req, const void *q,
+                          const void *k, const void *v, int32_t qkv_dtype, const float *alpha,
+                          const float *beta, float *o, void *stream);
+
+/* ------------------------------------------------------------------ prompts
+ *
+ * The prompt form of the recurrent layers: every token of n_seq sequences
+ * through the state, for a state computed where the decode steps will go on
+ * from it (pass S to sq_pool_store).  Sequence s is the packed tokens
+ * [cu_seqlens[s], cu_seqlens[s + 1]); per token t and head h
+ *     SQ_RULE_DELTA    S_t = alpha_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T
+ *     SQ_RULE_LINEAR   S_t = alpha_t S_{t-1} + beta_t k_t v_t^T
+ *     o_t = S_t^T q_t
+ * from S0 (or zero).  States, gates, sums and the products that feed a state
+ * are fp32 or better; o is rounded once to its type. */
+typedef enum {
+    SQ_RULE_DELTA = 0, /* the rule of sq_decode_step */
+    SQ_RULE_LINEAR = 1 /* the rule of sq_decode_step_linear */
+} sq_rule;
+
+typedef struct {
+    int32_t n_seq;             /* sequences, >= 0 */
+    int32_t n_tokens;          /* packed tokens of all sequences, >= 0 */
+    int32_t n_heads;           /* value (and state) heads, >= 1 */
+    int32_t n_k_heads;         /* query/key heads, a divisor of n_heads: head h
+                                  reads query/key head h / (n_heads / n_k_heads) */
+    int32_t d_k, d_v;          /* multiples of 4, at most 256 */
+    int32_t dtype;             /* sq_dtype of q, k, v and o */
+    int32_t rule;              /* sq_rule */
+    const void *q, *k;         /* DEVICE [n_tokens][n_k_heads][d_k] */
+    const void *v;             /* DEVICE [n_tokens][n_heads][d_v] */
+    int64_t q_stride, k_stride, v_stride; /* elements between tokens (heads are
+                                  contiguous inside a token), so that q, k and v
+                                  may be parts of one wider buffer */
+    const float *alpha, *beta; /* DEVICE fp32 [n_tokens][n_heads]: gate in [0, 1], write strength */
+    const int32_t *cu_seqlens; /* DEVICE int32 [n_seq + 1], from 0 to n_tokens, never falling
+                                  (equal neighbours are an empty sequence: S = S0) */
+    const float *S0;           /* DEVICE fp32 [n_seq][n_heads][d_k][d_v], or NULL for zero */
+    void *o;                   /* DEVICE [n_tokens][n_heads][d_v] of dtype */
+    float *S;                  /* DEVICE fp32 [n_seq][n_heads][d_k][d_v], or NULL; may equal S0 */
+    void *workspace;           /* DEVICE, 256-byte aligned, sq_prefill_workspace bytes; may be
+                                  NULL where that is 0 */
+    uint64_t workspace_bytes;
+} sq_prefill_desc;
+
+/* Bytes of workspace that sq_prefill needs for these sizes (0 if none, or if
+ * an argument is invalid).  It grows with n_seq, n_tokens and n_heads: one
+ * made for the largest call serves the smaller ones.  Host only. */
+uint64_t sq_prefill_workspace(int32_t n_seq, int32_t n_tokens, int32_t n_heads, int32_t d_k,
+                              int32_t d_v, int32_t dtype, int32_t rule);
+
+/* Run the prompt form (above).  n_seq == 0 is a no-op; with n_tokens == 0, S
+ * receives S0 (or zero).  Asynchronous on `stream`; the workspace is in use until
+ * the call's work is done.  cu_seqlens is read on the device only: values
+ * outside [0, n_tokens] are held to that range, nothing outside the buffers
+ * is touched, but tokens that it assigns to two sequences, or to none, have
+ * undefined outputs.  bfloat16 with d_k = d_v = 128, strides in multiples of
+ * 8 elements and 16-byte aligned q, k, v, o takes the chunked matrix kernels,
+ * everything else a token-by-token one.  Errors: SQ_ERR_INVALID (null
+ * or misaligned pointer, bad size, stride or enum, workspace too small),
+ * SQ_ERR_UNSUPPORTED (d_k or d_v, or more tiles than one launch grid),
+ * SQ_ERR_HIP. */
+int sq_prefill(const sq_prefill_desc *desc, void *stream);
+
+/* ------------------------------------------------------------- paged cache
+ *
+ * A key-value cache in pages of page_size tokens, for the softmax-attention
+ * layers of a hybrid model.  Token position x of a request lies in page
+ * block_table[request][x / page_size] at place x % page_size; its slot is
+ * page * page_size + place.  FORMAT (public): keys
+ *     k [n_pages][n_kv_heads][page_size][head_dim]
+ * and values transposed inside the page,
+ *     v [n_pages][n_kv_heads][head_dim][page_size]
+ * (the order in which attention's second product takes them).  Pages may lie
+ * anywhere in the pool and hold anything past a request's last token. */
+typedef struct {
+    void *k, *v;         /* DEVICE, 16-byte aligned; borrowed */
+    int32_t n_pages;     /* >= 1 */
+    int32_t page_size;   /* 16, 32, 64, 128 or 256 tokens */
+    int32_t n_kv_heads;  /* >= 1 */
+    int32_t head_dim;    /* 32, 64, 96, 128, 192 or 256 */
+    int32_t dtype;       /* sq_dtype of the cache, and of the q, k, v, o that go with it */
+} sq_kv_cache;
+
+/* Block tables and slot maps of one step from the requests' lengths.  Request
+ * i has ctx_lens[i] cached tokens and gets new_lens[i] more (both DEVICE int32
+ * [n_req]); with P = page_size it holds ceil(ctx / P) pages, listed at the
+ * start of its row, and needs ceil((ctx + new) / P).  All outputs DEVICE:
+ *   block_table int32 [n_req][table_stride]: the missing pages are appended
+ *               to each row, taken from free_pages (int32 [n_free]) in request
+ *               order: request 0 takes the first ones; other entries stay;
+ *   seq_lens    int32 [n_req]: ctx + new;
+ *   cu_new      int32 [n_req + 1]: exclusive sums of new_lens (the cu_seqlens
+ *               of sq_prefill);
+ *   cu_pages    int32 [n_req + 1]: exclusive sums of the pages taken; the last
+ *               entry is how many entries of free_pages are used up;
+ *   slot_map    int64 [n_slots]: the slot of every new token, requests packed
+ *               in order; entries after the last token are -1 (n_slots may
+ *               be any capacity, for instance that of a captured graph);
+ *   result      int32 [1]: 0, or a sum of 1 (a negative length, or more than
+ *               2^31 - 1 tokens: the request is taken as empty), 2 (n_free
+ *               pages are not enough), 4 (a row needs more than table_stride
+ *               entries), 8 (n_slots is less than the new tokens).  Pages that
+ *               are not to be had get -1 entries, their tokens slot -1.
+ * Nothing is kept between calls.  n_req == 0 writes the two zero sums.
+ * seq_lens, cu_new and cu_pages must not overlap the inputs.
+ * Errors: SQ_ERR_INVALID (null or misaligned pointer, negative size, n_slots
+ * above 2^31 - 1), SQ_ERR_UNSUPPORTED (page_size), SQ_ERR_HIP.  Asynchronous
+ * on `stream`. */
+int sq_block_tables(const int32_t *ctx_lens, const int32_t *new_lens, int32_t n_req,
+                    int32_t page_size, const int32_t *free_pages, int32_t n_free,
+                    int32_t *block_table, int64_t table_stride, int32_t *seq_lens, int32_t *cu_new,
+                    int32_t *cu_pages, int64_t *slot_map, int64_t n_slots, int32_t *result,
+                    void *stream);
+
+/* Write the keys and values of n_tok tokens into the cache at slot_map[t]
+ * (DEVICE int64 [n_tok]); a slot that is negative or past the cache is
+ * skipped, and no slot may appear twice.  k, v: DEVICE
+ * [n_tok][n_kv_heads][head_dim] of the cache's type, 16-byte aligned, tokens
+ * k_stride / v_stride elements apart (a multiple of 16 bytes).  n_tok == 0 is a
+ * no-op.  `cache` is a HOST struct, read during the call.
+ * Errors: SQ_ERR_INVALID, SQ_ERR_UNSUPPORTED (page_size, head_dim, too many
+ * tokens for a launch grid), SQ_ERR_HIP.  Asynchronous on `stream`. */
+int sq_kv_append(const sq_kv_cache *cache, const void *k, const void *v, int64_t k_stride,
+                 int64_t v_stride, const int64_t *slot_map, int32_t n_tok, void *stream);
+
+/* Bytes of workspace for sq_paged_attention with at most n_req requests of at
+ * most max_len tokens and any window (0 if none, or if an argument is
+ * invalid).  Host only. */
+uint64_t sq_paged_attention_workspace(const sq_kv_cache *cache, int32_t n_req, int32_t n_heads,
+                                      int32_t max_len);
+
+/* Attention of one new token per request over its cached tokens (the new
+ * token's own key and value appended before):
+ *     o[r][h] = sum_x p_x v_x,  p = softmax over x of scale q[r][h] . k_x,
+ * x over the request's last `window` tokens (0: all) of seq_lens[r], query
+ * head h reading key-value head h / (n_heads / n_kv_heads).
+ *   q   DEVICE [n_req][n_heads][head_dim] of the cache's type, requests
+ *       q_stride elements apart (a multiple of 16 bytes);
+ *   block_table, seq_lens  DEVICE int32, as sq_block_tables writes them;
+ *   max_len   HOST upper bound of seq_lens (it sets how the context is split
+ *       over workgroups); a longer request is cut to its first max_len tokens;
+ *   o   DEVICE [n_req][n_heads][head_dim] of the cache's type;
+ *   lse DEVICE fp32 [n_req][n_heads], or NULL: log sum exp(scale q . k_x).
+ * A request without tokens gets o = 0 and lse = -inf.  Table entries outside
+ * the cache are read as absent tokens.  Keys and values past seq_lens are not
+ * used, whatever they hold.  Sums and the softmax are fp32.  n_req == 0 is a
+ * no-op.  Errors: SQ_ERR_INVALID (null or misaligned pointer, bad size,
+ * workspace too small), SQ_ERR_UNSUPPORTED (page_size, head_dim, launch grid),
+ * SQ_ERR_HIP.  Asynchronous on `stream`; the workspace is in use until the
+ * call's work is done. */
+int sq_paged_attention(const sq_kv_cache *cache, const void *q, int64_t q_stride, int32_t n_req,
+                       int32_t n_heads, const int32_t *block_table, int64_t table_stride,
+                       const int32_t *seq_lens, int32_t max_len, float scale, int32_t window,
+                       void *o, float *lse, void *workspace, uint64_t workspace_bytes, void *stream);
+
 /* Readout without update ([P5] 空间维度: the head's output is the query read
  * out of the state): o = S^T q from the stored state (dequantized), for
  * slots slot_ids[0..n_req).  q: DEVICE [n_req][n_heads][d_k] of q_dtype;

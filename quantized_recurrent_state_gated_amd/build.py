@@ -11,7 +11,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libsq.so")
-SOURCES = ["sq_kernels.hip", "sq_api.hip"]
+SOURCES = ["sq_kernels.hip", "sq_api.hip", "sq_paged.hip", "sq_prefill.hip", "sq_serve_api.hip"]
 ARCH = os.environ.get("SQ_OFFLOAD_ARCH", "gfx950")
 
 

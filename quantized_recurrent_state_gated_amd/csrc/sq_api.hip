@@ -302,7 +302,8 @@ static int run_classes(const sq_pool *p, sqk::Op op, sqk::StepArgs a, bool bf16,
     // per wide class (FP32, BF16 states); otherwise one launch per width
     // class, widest tiles first
     static const int order[kNumClasses] = {kClassF32, kClassBF16, 3, 2, 1, 0};
-    const bool step_or_read = op == sqk::OP_STEP || op == sqk::OP_STEP_KDA || op == sqk::OP_READOUT;
+    const bool step_or_read = op == sqk::OP_STEP || op == sqk::OP_STEP_KDA ||
+                              op == sqk::OP_STEP_LINEAR || op == sqk::OP_READOUT;
     if (step_or_read && p->dk == 128 && p->dv == 128 && !p->generic) {
         const uint64_t total = tiles;
         if (p->n_class[kClassF32] + p->n_class[kClassBF16] < p->n_heads) {  // any 4/6/8/16-bit heads
@@ -359,9 +360,10 @@ int sq_pool_load(const sq_pool *pool, const int32_t *slot_ids, int32_t n_req, fl
     return run_classes(pool, sqk::OP_LOAD, a, false, n_req, stream);
 }
 
-int sq_decode_step(sq_pool *pool, const int32_t *slot_ids, int32_t n_req, const void *q,
-                   const void *k, const void *v, int32_t qkv_dtype, const float *alpha,
-                   const float *beta, float *o, void *stream)
+// the two steps whose gate is one value per request and head
+static int step_scalar_gate(sq_pool *pool, sqk::Op op, const int32_t *slot_ids, int32_t n_req,
+                            const void *q, const void *k, const void *v, int32_t qkv_dtype,
+                            const float *alpha, const float *beta, float *o, void *stream)
 {
     if (!pool || n_req < 0) return SQ_ERR_INVALID;
     if (qkv_dtype != SQ_F32 && qkv_dtype != SQ_BF16) return SQ_ERR_INVALID;
@@ -379,7 +381,23 @@ int sq_decode_step(sq_pool *pool, const int32_t *slot_ids, int32_t n_req, const 
     a.alpha = alpha;
     a.beta = beta;
     a.o = o;
-    return run_classes(pool, sqk::OP_STEP, a, qkv_dtype == SQ_BF16, n_req, stream);
+    return run_classes(pool, op, a, qkv_dtype == SQ_BF16, n_req, stream);
+}
+
+int sq_decode_step(sq_pool *pool, const int32_t *slot_ids, int32_t n_req, const void *q,
+                   const void *k, const void *v, int32_t qkv_dtype, const float *alpha,
+                   const float *beta, float *o, void *stream)
+{
+    return step_scalar_gate(pool, sqk::OP_STEP, slot_ids, n_req, q, k, v, qkv_dtype, alpha, beta, o,
+                            stream);
+}
+
+int sq_decode_step_linear(sq_pool *pool, const int32_t *slot_ids, int32_t n_req, const void *q,
+                          const void *k, const void *v, int32_t qkv_dtype, const float *alpha,
+                          const float *beta, float *o, void *stream)
+{
+    return step_scalar_gate(pool, sqk::OP_STEP_LINEAR, slot_ids, n_req, q, k, v, qkv_dtype, alpha,
+                            beta, o, stream);
 }
 
 int sq_decode_step_kda(sq_pool *pool, const int32_t *slot_ids, int32_t n_req, const void *q,

@@ -27,7 +27,14 @@
 // S' = (I - beta k k^T) diag(alpha) Shat + beta k v^T, alpha in R^{d_k}) is
 // the same arithmetic with alpha_i moved into the row factors: u and y use
 // weights alpha_i k_i r_i and alpha_i q_i r_i, the column terms take alpha = 1,
-// and the requantization uses alpha_i per row.  Template flag CHG.
+// and the requantization uses alpha_i per row.  Template mode kChannel.
+//
+// The plain-decay step S' = alpha Shat + beta k v^T has no correction along
+// the key: the same arithmetic without u, so b_j = v_j / c_j and
+// o_j = alpha y_j + beta (q.k) v_j.  Template mode kDecay.  FP32 and BF16
+// states take S' with each product and the sum rounded by itself
+// (decay_write): any evaluation of the formula as written gives those bits,
+// where a fused multiply-add moves about one BF16 rounding in 2^15.
 #include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
 #include <mutex>
@@ -38,6 +45,10 @@
 #include "sq_launch.h"
 
 namespace sqk {
+
+// How a step decays the state: one gate per head (delta rule), one per key
+// channel (delta rule), or one per head with no delta correction.
+enum StepMode { kScalar = 0, kChannel = 1, kDecay = 2 };
 
 // ---------------------------------------------------------------- loads
 
@@ -67,6 +78,14 @@ __device__ __forceinline__ void ld4<uint16_t>(const uint16_t *p, long i, float (
     x[1] = __uint_as_float(u.x & 0xffff0000u);
     x[2] = __uint_as_float(u.y << 16);
     x[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+
+// alpha S + w v, rounded after each operation (no fused multiply-add)
+__device__ __forceinline__ float decay_write(float alpha, float S, float wv)
+{
+#pragma clang fp contract(off)
+    const float x = alpha * S;
+    return x + wv;
 }
 
 // ---------------------------------------------------------------- block codec
@@ -432,9 +451,10 @@ struct SmemWideK : SmemWide {
 // with 256, 3.88 with 128, 3.94 with 512; BF16 1.93-1.96 ms for all three)
 constexpr int kWideTPB = 256;
 
-template <int FMT, typename T, bool UPDATE, bool CHG, typename SM>
+template <int FMT, typename T, bool UPDATE, int MODE, typename SM>
 __device__ __forceinline__ void tile128_wide(const StepArgs &a, int n, int h, SM &sm)
 {
+    constexpr bool CHG = MODE == kChannel, LIN = MODE == kDecay;
     static_assert(FMT == 32 || FMT == kBF16, "unquantized states only");
     constexpr int E = FMT == 32 ? 4 : 2;        // bytes per element
     constexpr int CPL = 4 / E;                  // columns per lane
@@ -512,14 +532,14 @@ __device__ __forceinline__ void tile128_wide(const StepArgs &a, int n, int h, SM
 #pragma unroll
             for (int c = 0; c < CPL; c++) {
                 const float x = elem(m, r, c);
-                if (UPDATE) pu[c] = fmaf(wr[r], x, pu[c]);
+                if (UPDATE && !LIN) pu[c] = fmaf(wr[r], x, pu[c]);
                 py[c] = fmaf(gr[r], x, py[c]);
             }
     }
     const int j0 = CPL * (64 * ch + lane);  // the lane's first column
 #pragma unroll
     for (int c = 0; c < CPL; c++) {
-        sm.red[rgp][0][j0 + c] = pu[c];
+        if (!LIN) sm.red[rgp][0][j0 + c] = pu[c];
         sm.red[rgp][1][j0 + c] = py[c];
     }
     __syncthreads();
@@ -529,14 +549,14 @@ __device__ __forceinline__ void tile128_wide(const StepArgs &a, int n, int h, SM
         float U = 0.0f, Y = 0.0f;
 #pragma unroll
         for (int r = 0; r < NRG; r++) {
-            U += sm.red[r][0][t];
+            if (!LIN) U += sm.red[r][0][t];
             Y += sm.red[r][1][t];
         }
         const float qk = sm.sum[0][0] + sm.sum[1][0];
         if (!UPDATE) {
             a.o[nh * 128 + t] = Y;
         } else {
-            const float e = sm.vc[t].x - alpha * U;
+            const float e = LIN ? sm.vc[t].x : sm.vc[t].x - alpha * U;
             if (a.o) a.o[nh * 128 + t] = fmaf(alpha, Y, beta * qk * e);
             sm.b[t] = e;
         }
@@ -567,7 +587,8 @@ __device__ __forceinline__ void tile128_wide(const StepArgs &a, int n, int h, SM
             }
 #pragma unroll
             for (int c = 0; c < CPL; c++) {
-                z[r][c] = fmaf(gi, elem(m, r, c), ai * b[c]);
+                z[r][c] = LIN ? decay_write(gi, elem(m, r, c), ai * b[c])
+                              : fmaf(gi, elem(m, r, c), ai * b[c]);
                 nf |= !__builtin_isfinite(z[r][c]);
             }
         }
@@ -918,9 +939,10 @@ struct SmemFusedK : SmemFused {
     alignas(16) float4 pa[128];
 };
 
-template <int BITS, typename T, bool UPDATE, bool CHG, int TPB, typename SM>
+template <int BITS, typename T, bool UPDATE, int MODE, int TPB, typename SM>
 __device__ __forceinline__ void tile128(const StepArgs &a, uint32_t n, uint32_t h, SM &sm)
 {
+    constexpr bool CHG = MODE == kChannel, LIN = MODE == kDecay;
     // TPB threads per tile: RG = TPB / 32 row groups, MB = 32 / RG blocks per thread
     constexpr int RG = TPB / 32, MB = 32 / RG;
     static_assert(TPB == 128 || TPB == 256, "128 or 256 threads per tile");
@@ -1012,20 +1034,20 @@ __device__ __forceinline__ void tile128(const StepArgs &a, uint32_t n, uint32_t 
             for (int cj = 0; cj < 4; cj++) {
                 const int e = 4 * cj + ri;
                 const float x = half_of(hv[m][P::k(e)], P::sel(e));
-                if (UPDATE) pu[cj] = fmaf(wr[ri], x, pu[cj]);
+                if (UPDATE && !LIN) pu[cj] = fmaf(wr[ri], x, pu[cj]);
                 py[cj] = fmaf(gr[ri], x, py[cj]);
             }
     }
-    if (UPDATE) *reinterpret_cast<float4 *>(&sm.red[rg][0][4 * cb]) = make_float4(pu[0], pu[1], pu[2], pu[3]);
+    if (UPDATE && !LIN) *reinterpret_cast<float4 *>(&sm.red[rg][0][4 * cb]) = make_float4(pu[0], pu[1], pu[2], pu[3]);
     *reinterpret_cast<float4 *>(&sm.red[rg][1][4 * cb]) = make_float4(py[0], py[1], py[2], py[3]);
     __syncthreads();
 
     // column finalisation: thread j < 128 owns column j
     if (t < 128) {
-        float U = UPDATE ? sm.red[0][0][t] : 0.0f, Y = sm.red[0][1][t];
+        float U = UPDATE && !LIN ? sm.red[0][0][t] : 0.0f, Y = sm.red[0][1][t];
 #pragma unroll
         for (int r = 1; r < RG; r++) {
-            if (UPDATE) U += sm.red[r][0][t];
+            if (UPDATE && !LIN) U += sm.red[r][0][t];
             Y += sm.red[r][1][t];
         }
         const float4 s0 = *reinterpret_cast<const float4 *>(&sm.sum[0][0]);
@@ -1037,7 +1059,7 @@ __device__ __forceinline__ void tile128(const StepArgs &a, uint32_t n, uint32_t 
             a.o[nh * 128 + t] = yj;
         } else {
             const float uj = cj * (U - OFF * (s0.y + s1.y));
-            const float e = vc.x - alpha * uj;
+            const float e = LIN ? vc.x : vc.x - alpha * uj;
             if (a.o) a.o[nh * 128 + t] = fmaf(alpha, yj, beta * (s0.x + s1.x) * e);
             const float bj = QUANT ? e * __builtin_amdgcn_rcpf(cj) : e;
             sm.b[t] = bj;
@@ -1120,22 +1142,22 @@ __device__ __forceinline__ void tile128(const StepArgs &a, uint32_t n, uint32_t 
     if (__ballot(nf) && (t & 63) == 0) a.err[0] = 1;
 }
 
-template <typename T, bool UPDATE, bool CHG, int TPB, int WPE>
+template <typename T, bool UPDATE, int MODE, int TPB, int WPE>
 __global__ __launch_bounds__(TPB) __attribute__((amdgpu_waves_per_eu(WPE, 8))) void k_step128(FusedArgs f)
 {
     // tile b is request b / H, head b % H: each XCD walks its part of the pool
     // in memory order, so tiles of every width are interleaved on each CU
     // (VALU-heavy narrow codes overlap with memory-heavy wide tiles).  FP32-
     // and BF16-state heads are skipped here and run in k_step128_wide.
-    using SM = typename std::conditional<CHG, SmemFusedK, SmemFused>::type;
+    using SM = typename std::conditional<MODE == kChannel, SmemFusedK, SmemFused>::type;
     __shared__ SM sm;
     uint32_t n, h;
     if (!xcd_tile((uint32_t)f.a.n_req, (uint32_t)f.a.H, f.a.xm, n, h)) return;
     switch (sload(f.head_bits + h)) {
-    case 16: tile128<16, T, UPDATE, CHG, TPB>(f.a, n, h, sm); break;
-    case 8: tile128<8, T, UPDATE, CHG, TPB>(f.a, n, h, sm); break;
-    case 6: tile128<6, T, UPDATE, CHG, TPB>(f.a, n, h, sm); break;
-    case 4: tile128<4, T, UPDATE, CHG, TPB>(f.a, n, h, sm); break;
+    case 16: tile128<16, T, UPDATE, MODE, TPB>(f.a, n, h, sm); break;
+    case 8: tile128<8, T, UPDATE, MODE, TPB>(f.a, n, h, sm); break;
+    case 6: tile128<6, T, UPDATE, MODE, TPB>(f.a, n, h, sm); break;
+    case 4: tile128<4, T, UPDATE, MODE, TPB>(f.a, n, h, sm); break;
     default: break;
     }
 }
@@ -1145,32 +1167,32 @@ __global__ __launch_bounds__(TPB) __attribute__((amdgpu_waves_per_eu(WPE, 8))) v
 // barrier, and a half with no tile, or an FP32/BF16 head, simply ends).
 // Measured on full serving launches: a memory-only copy of the step moves its
 // bytes 5-6 % faster with two tiles per workgroup than with one.
-template <typename T, bool UPDATE, bool CHG, int WPE>
+template <typename T, bool UPDATE, int MODE, int WPE>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WPE, 8))) void k_step128x2(FusedArgs f)
 {
-    using SM = typename std::conditional<CHG, SmemFusedK, SmemFused>::type;
+    using SM = typename std::conditional<MODE == kChannel, SmemFusedK, SmemFused>::type;
     __shared__ SM sm[2];
     const uint32_t half = __builtin_amdgcn_readfirstlane(threadIdx.x >> 7);  // uniform per wave
     uint32_t n, h;
     if (!xcd_tile_pair((uint32_t)f.a.n_req, (uint32_t)f.a.H, f.a.xm, half, n, h)) return;
     switch (sload(f.head_bits + h)) {
-    case 16: tile128<16, T, UPDATE, CHG, 128>(f.a, n, h, sm[half]); break;
-    case 8: tile128<8, T, UPDATE, CHG, 128>(f.a, n, h, sm[half]); break;
-    case 6: tile128<6, T, UPDATE, CHG, 128>(f.a, n, h, sm[half]); break;
-    case 4: tile128<4, T, UPDATE, CHG, 128>(f.a, n, h, sm[half]); break;
+    case 16: tile128<16, T, UPDATE, MODE, 128>(f.a, n, h, sm[half]); break;
+    case 8: tile128<8, T, UPDATE, MODE, 128>(f.a, n, h, sm[half]); break;
+    case 6: tile128<6, T, UPDATE, MODE, 128>(f.a, n, h, sm[half]); break;
+    case 4: tile128<4, T, UPDATE, MODE, 128>(f.a, n, h, sm[half]); break;
     default: break;
     }
 }
 
-template <int FMT, typename T, bool UPDATE, bool CHG>
+template <int FMT, typename T, bool UPDATE, int MODE>
 __global__ __launch_bounds__(kWideTPB) void k_step128_wide(StepArgs a)
 {
     // FP32- or BF16-state heads of a d = 128 pool (a.heads / a.Hc)
-    using SM = typename std::conditional<CHG, SmemWideK, SmemWide>::type;
+    using SM = typename std::conditional<MODE == kChannel, SmemWideK, SmemWide>::type;
     __shared__ SM sm;
     uint32_t n, hc;
     if (!xcd_tile((uint32_t)a.n_req, (uint32_t)a.Hc, a.xm, n, hc)) return;
-    tile128_wide<FMT, T, UPDATE, CHG>(a, (int)n, a.heads[hc], sm);
+    tile128_wide<FMT, T, UPDATE, MODE>(a, (int)n, a.heads[hc], sm);
 }
 
 // ---------------------------------------------------------------- any shape
@@ -1201,9 +1223,10 @@ __device__ __forceinline__ float field_value(uint32_t f)
     else return __uint_as_float(f);
 }
 
-template <int BITS, typename T, bool UPDATE, bool CHG>
+template <int BITS, typename T, bool UPDATE, int MODE>
 __global__ __launch_bounds__(256) void k_tile_any(StepArgs a)
 {
+    constexpr bool CHG = MODE == kChannel, LIN = MODE == kDecay;
     constexpr int W = fw<BITS>() / 2;
     constexpr bool QUANT = BITS <= 8;
     constexpr float OFF = QUANT ? (float)(1 << (BITS - 1)) : 0.0f;
@@ -1256,7 +1279,8 @@ __global__ __launch_bounds__(256) void k_tile_any(StepArgs a)
             a.o[nh * dv + j] = yj;
             continue;
         }
-        const float e = ld1(v, nh * dv + j) - alpha * uj;
+        const float vj = ld1(v, nh * dv + j);
+        const float e = LIN ? vj : vj - alpha * uj;
         if (a.o) a.o[nh * dv + j] = fmaf(alpha, yj, beta * sQK * e);
         sB[j] = QUANT ? e / cj : e;
     }
@@ -1277,7 +1301,11 @@ __global__ __launch_bounds__(256) void k_tile_any(StepArgs a)
 #pragma unroll
             for (int ri = 0; ri < 4; ri++) {
                 const float g = sL[i0 + ri];
-                float x = fmaf(g, f[4 * cj + ri], fmaf(sA[i0 + ri], sB[j0 + cj], OFF * (1.0f - g)));
+                float x;
+                if constexpr (LIN && BITS >= 32)
+                    x = decay_write(g, f[4 * cj + ri], sA[i0 + ri] * sB[j0 + cj]);
+                else
+                    x = fmaf(g, f[4 * cj + ri], fmaf(sA[i0 + ri], sB[j0 + cj], OFF * (1.0f - g)));
                 nf |= !__builtin_isfinite(x);
                 if (QUANT && x != x) x = OFF;  // a NaN becomes code 0
                 z[4 * cj + ri] = x;
@@ -1408,11 +1436,13 @@ static hipError_t launch_bits(Op op, const StepArgs &a, int32_t n_req, hipStream
     }
     const dim3 grid((unsigned)((long)n_req * a.Hc));
     if (op == OP_STEP)
-        hipLaunchKernelGGL((k_tile_any<BITS, T, true, false>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((k_tile_any<BITS, T, true, kScalar>), grid, dim3(256), 0, st, a);
     else if (op == OP_STEP_KDA)
-        hipLaunchKernelGGL((k_tile_any<BITS, T, true, true>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((k_tile_any<BITS, T, true, kChannel>), grid, dim3(256), 0, st, a);
+    else if (op == OP_STEP_LINEAR)
+        hipLaunchKernelGGL((k_tile_any<BITS, T, true, kDecay>), grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((k_tile_any<BITS, T, false, false>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((k_tile_any<BITS, T, false, kScalar>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
@@ -1434,11 +1464,13 @@ template <int FMT, typename T>
 static void wide128_t(Op op, const StepArgs &a, dim3 grid, hipStream_t st)
 {
     if (op == OP_STEP)
-        hipLaunchKernelGGL((k_step128_wide<FMT, T, true, false>), grid, dim3(kWideTPB), 0, st, a);
+        hipLaunchKernelGGL((k_step128_wide<FMT, T, true, kScalar>), grid, dim3(kWideTPB), 0, st, a);
     else if (op == OP_STEP_KDA)
-        hipLaunchKernelGGL((k_step128_wide<FMT, T, true, true>), grid, dim3(kWideTPB), 0, st, a);
+        hipLaunchKernelGGL((k_step128_wide<FMT, T, true, kChannel>), grid, dim3(kWideTPB), 0, st, a);
+    else if (op == OP_STEP_LINEAR)
+        hipLaunchKernelGGL((k_step128_wide<FMT, T, true, kDecay>), grid, dim3(kWideTPB), 0, st, a);
     else
-        hipLaunchKernelGGL((k_step128_wide<FMT, T, false, false>), grid, dim3(kWideTPB), 0, st, a);
+        hipLaunchKernelGGL((k_step128_wide<FMT, T, false, kScalar>), grid, dim3(kWideTPB), 0, st, a);
 }
 
 hipError_t launch_wide128(Op op, int bits, bool qkv_bf16, const StepArgs &a, int32_t n_req,
@@ -1465,11 +1497,13 @@ template <typename T, int TPB, int WPE>
 static void fused128_t(Op op, const FusedArgs &f, dim3 grid, hipStream_t st)
 {
     if (op == OP_STEP)
-        hipLaunchKernelGGL((k_step128<T, true, false, TPB, WPE>), grid, dim3(TPB), 0, st, f);
+        hipLaunchKernelGGL((k_step128<T, true, kScalar, TPB, WPE>), grid, dim3(TPB), 0, st, f);
     else if (op == OP_STEP_KDA)
-        hipLaunchKernelGGL((k_step128<T, true, true, TPB, WPE>), grid, dim3(TPB), 0, st, f);
+        hipLaunchKernelGGL((k_step128<T, true, kChannel, TPB, WPE>), grid, dim3(TPB), 0, st, f);
+    else if (op == OP_STEP_LINEAR)
+        hipLaunchKernelGGL((k_step128<T, true, kDecay, TPB, WPE>), grid, dim3(TPB), 0, st, f);
     else
-        hipLaunchKernelGGL((k_step128<T, false, false, TPB, WPE>), grid, dim3(TPB), 0, st, f);
+        hipLaunchKernelGGL((k_step128<T, false, kScalar, TPB, WPE>), grid, dim3(TPB), 0, st, f);
 }
 
 template <int TPB, int WPE>
@@ -1483,11 +1517,13 @@ template <typename T>
 static void fused128x2_t(Op op, const FusedArgs &f, dim3 grid, hipStream_t st)
 {
     if (op == OP_STEP)
-        hipLaunchKernelGGL((k_step128x2<T, true, false, 5>), grid, dim3(256), 0, st, f);
+        hipLaunchKernelGGL((k_step128x2<T, true, kScalar, 5>), grid, dim3(256), 0, st, f);
     else if (op == OP_STEP_KDA)
-        hipLaunchKernelGGL((k_step128x2<T, true, true, 5>), grid, dim3(256), 0, st, f);
+        hipLaunchKernelGGL((k_step128x2<T, true, kChannel, 5>), grid, dim3(256), 0, st, f);
+    else if (op == OP_STEP_LINEAR)
+        hipLaunchKernelGGL((k_step128x2<T, true, kDecay, 5>), grid, dim3(256), 0, st, f);
     else
-        hipLaunchKernelGGL((k_step128x2<T, false, false, 5>), grid, dim3(256), 0, st, f);
+        hipLaunchKernelGGL((k_step128x2<T, false, kScalar, 5>), grid, dim3(256), 0, st, f);
 }
 
 // tile counts that take the 256-thread launch (four waves per tile); larger

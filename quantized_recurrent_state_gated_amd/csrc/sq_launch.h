@@ -30,8 +30,9 @@ struct StepArgs {
     uint32_t xm[8];            // reciprocals for the XCD-aware tile order (set by the launchers)
 };
 
-// OP_STEP_KDA is the step with a per-key-channel gate (alpha [n_req][H][dk]).
-enum Op { OP_STEP = 0, OP_READOUT = 1, OP_STORE = 2, OP_LOAD = 3, OP_STEP_KDA = 4 };
+// OP_STEP_KDA is the step with a per-key-channel gate (alpha [n_req][H][dk]),
+// OP_STEP_LINEAR the step without the delta correction.
+enum Op { OP_STEP = 0, OP_READOUT = 1, OP_STORE = 2, OP_LOAD = 3, OP_STEP_KDA = 4, OP_STEP_LINEAR = 5 };
 
 // One launch over every tile of a d_k = d_v = 128 pool: tile b is request
 // b / H, head b % H, whose width is head_bits[h].

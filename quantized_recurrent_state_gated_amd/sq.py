@@ -27,7 +27,9 @@ SQ_F32, SQ_BF16 = 0, 1
 EXPORTED = ("sq_pool_bytes", "sq_pool_alloc", "sq_pool_free", "sq_pool_tile_offset",
             "sq_pool_store", "sq_pool_load", "sq_decode_step", "sq_decode_step_kda", "sq_readout",
             "sq_check_slots", "sq_check_slots_noalloc", "sq_pool_last_device_error",
-            "sq_status_string")
+            "sq_status_string", "sq_decode_step_linear", "sq_prefill", "sq_prefill_workspace",
+            "sq_block_tables", "sq_kv_append", "sq_paged_attention", "sq_paged_attention_workspace")
+SQ_RULE_DELTA, SQ_RULE_LINEAR = 0, 1
 
 
 class SqPoolDesc(ctypes.Structure):
@@ -39,7 +41,24 @@ class SqPoolDesc(ctypes.Structure):
                 ("state", ctypes.c_void_p), ("state_bytes", ctypes.c_uint64)]
 
 
+class SqPrefillDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_seq", "n_tokens", "n_heads", "n_k_heads", "d_k",
+                                               "d_v", "dtype", "rule")]
+                + [(n, ctypes.c_void_p) for n in ("q", "k", "v")]
+                + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")]
+                + [(n, ctypes.c_void_p) for n in ("alpha", "beta", "cu_seqlens", "S0", "o", "S",
+                                                  "workspace")]
+                + [("workspace_bytes", ctypes.c_uint64)])
+
+
+class SqKvCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
 _vp, _i32 = ctypes.c_void_p, ctypes.c_int32
+_i64, _u64 = ctypes.c_int64, ctypes.c_uint64
 _lib.sq_pool_bytes.restype = ctypes.c_uint64
 _lib.sq_pool_bytes.argtypes = [_i32, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_uint8)]
 _lib.sq_pool_alloc.restype = ctypes.c_int
@@ -57,6 +76,22 @@ _lib.sq_decode_step.restype = ctypes.c_int
 _lib.sq_decode_step.argtypes = [_vp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp]
 _lib.sq_decode_step_kda.restype = ctypes.c_int
 _lib.sq_decode_step_kda.argtypes = [_vp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp]
+_lib.sq_decode_step_linear.restype = ctypes.c_int
+_lib.sq_decode_step_linear.argtypes = [_vp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp]
+_lib.sq_prefill_workspace.restype = _u64
+_lib.sq_prefill_workspace.argtypes = [_i32] * 7
+_lib.sq_prefill.restype = ctypes.c_int
+_lib.sq_prefill.argtypes = [ctypes.POINTER(SqPrefillDesc), _vp]
+_lib.sq_block_tables.restype = ctypes.c_int
+_lib.sq_block_tables.argtypes = [_vp, _vp, _i32, _i32, _vp, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
+                                 _vp, _vp]
+_lib.sq_kv_append.restype = ctypes.c_int
+_lib.sq_kv_append.argtypes = [ctypes.POINTER(SqKvCacheDesc), _vp, _vp, _i64, _i64, _vp, _i32, _vp]
+_lib.sq_paged_attention_workspace.restype = _u64
+_lib.sq_paged_attention_workspace.argtypes = [ctypes.POINTER(SqKvCacheDesc), _i32, _i32, _i32]
+_lib.sq_paged_attention.restype = ctypes.c_int
+_lib.sq_paged_attention.argtypes = [ctypes.POINTER(SqKvCacheDesc), _vp, _i64, _i32, _i32, _vp, _i64, _vp,
+                                    _i32, ctypes.c_float, _i32, _vp, _vp, _vp, _u64, _vp]
 _lib.sq_readout.restype = ctypes.c_int
 _lib.sq_readout.argtypes = [_vp, _vp, _i32, _vp, _i32, _vp, _vp]
 _lib.sq_check_slots.restype = ctypes.c_int
@@ -293,3 +328,162 @@ def sq_readout(pool: SqPool, slot_ids, q, o, stream=None) -> None:
     _arg(o, "sq_readout", "o", (torch.float32,), n_req * pool.n_heads * pool.d_v)
     _check(_lib.sq_readout(pool.handle, _ptr(slot_ids), n_req, _ptr(q), _dtype_code(q), _ptr(o),
                            _stream(stream)), "sq_readout")
+
+
+def sq_decode_step_linear(pool: SqPool, slot_ids, q, k, v, alpha, beta, o=None, stream=None) -> None:
+    """The step without the delta correction: S' = alpha S + beta k v^T, o = S'^T q."""
+    n_req = _step_args("sq_decode_step_linear", pool, slot_ids, q, k, v, alpha, beta, o, False)
+    _check(_lib.sq_decode_step_linear(pool.handle, _ptr(slot_ids), n_req, _ptr(q), _ptr(k), _ptr(v),
+                                      _dtype_code(q), _ptr(alpha), _ptr(beta), _ptr(o),
+                                      _stream(stream)), "sq_decode_step_linear")
+
+
+# ---------------------------------------------------------------- prompts, paged cache
+
+def _rows(x, where: str, name: str, dtype, shape) -> int:
+    """Check a [tokens][heads][d] tensor whose tokens may lie further apart
+    than their elements (a part of a wider buffer); returns that distance."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{where}: {name} must be a torch tensor")
+    if x.dtype != dtype:
+        raise TypeError(f"{where}: {name} must be {dtype}, got {x.dtype}")
+    if tuple(x.shape) != shape:
+        raise SqError(SQ_ERR_INVALID, f"{where} ({name} has shape {tuple(x.shape)}, expected {shape})")
+    row = shape[1] * shape[2]
+    if not x.numel():
+        return row
+    if x.device.type not in _DEVICE_TYPES:
+        raise SqError(SQ_ERR_INVALID, f"{where} ({name} is not on a GPU)")
+    st = x.stride()
+    if (shape[2] > 1 and st[2] != 1) or (shape[1] > 1 and st[1] != shape[2]):
+        raise SqError(SQ_ERR_INVALID, f"{where} (the heads of a token of {name} are not contiguous)")
+    return st[0] if shape[0] > 1 else row
+
+
+def sq_prefill_workspace(n_seq: int, n_tokens: int, n_heads: int, d_k: int, d_v: int, dtype,
+                         rule: int = SQ_RULE_DELTA) -> int:
+    """Bytes of workspace of sq_prefill; `dtype` is a torch dtype or an sq_dtype."""
+    code = {torch.bfloat16: SQ_BF16, torch.float32: SQ_F32}.get(dtype, dtype)
+    if not isinstance(code, int):
+        raise TypeError(f"sq_prefill_workspace: dtype must be float32 or bfloat16, got {dtype}")
+    return int(_lib.sq_prefill_workspace(n_seq, n_tokens, n_heads, d_k, d_v, code, rule))
+
+
+def sq_prefill(q, k, v, alpha, beta, cu_seqlens, o, S=None, S0=None, rule: int = SQ_RULE_DELTA,
+               workspace=None, stream=None) -> None:
+    """Packed prompts through the recurrent state.  q, k [N][Hk][dk], v and o
+    [N][H][dv] (float32 or bfloat16, tokens may be strided, o contiguous), alpha
+    and beta fp32 [N][H], cu_seqlens int32 [n_seq + 1], S0 and S fp32
+    [n_seq][H][dk][dv].  `workspace`: uint8, sq_prefill_workspace bytes."""
+    w = "sq_prefill"
+    if q.dim() != 3 or v.dim() != 3:
+        raise SqError(SQ_ERR_INVALID, f"{w} (q, k and v are [tokens][heads][d])")
+    code, dt = _dtype_code(q), q.dtype
+    N, Hk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    n_seq = int(cu_seqlens.numel()) - 1
+    qs = _rows(q, w, "q", dt, (N, Hk, dk))
+    ks = _rows(k, w, "k", dt, (N, Hk, dk))
+    vs = _rows(v, w, "v", dt, (N, H, dv))
+    _arg(alpha, w, "alpha", (torch.float32,), N * H)
+    _arg(beta, w, "beta", (torch.float32,), N * H)
+    _arg(cu_seqlens, w, "cu_seqlens", (torch.int32,), n_seq + 1)
+    _arg(o, w, "o", (dt,), N * H * dv)
+    _arg(S, w, "S", (torch.float32,), n_seq * H * dk * dv, optional=True)
+    _arg(S0, w, "S0", (torch.float32,), n_seq * H * dk * dv, optional=True)
+    ws, nb = _workspace(workspace, w)
+    d = SqPrefillDesc(n_seq, N, H, Hk, dk, dv, code, int(rule), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                      qs, ks, vs, _ptr(alpha), _ptr(beta), _ptr(cu_seqlens), _ptr(S0), _ptr(o), _ptr(S),
+                      ws, nb)
+    _check(_lib.sq_prefill(ctypes.byref(d), _stream(stream)), w)
+
+
+def _workspace(ws, where: str):
+    if ws is None:
+        return None, 0
+    if not isinstance(ws, torch.Tensor) or not ws.is_contiguous():
+        raise TypeError(f"{where}: workspace must be a contiguous torch tensor")
+    if ws.numel() and ws.device.type not in _DEVICE_TYPES:
+        raise SqError(SQ_ERR_INVALID, f"{where} (workspace is not on a GPU)")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+class SqKvCache:
+    """A paged key-value cache over two tensors: k [n_pages][n_kv_heads][page_size][head_dim],
+    v [n_pages][n_kv_heads][head_dim][page_size], float32 or bfloat16; keeps them alive."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        if k.dim() != 4:
+            raise SqError(SQ_ERR_INVALID, "SqKvCache (k is [n_pages][n_kv_heads][page_size][head_dim])")
+        pages, heads, page, d = k.shape
+        code = _dtype_code(k)
+        _arg(k, "SqKvCache", "k", _FLOATS, k.numel())
+        _arg(v, "SqKvCache", "v", (k.dtype,), k.numel())
+        if tuple(v.shape) != (pages, heads, d, page):
+            raise SqError(SQ_ERR_INVALID, "SqKvCache (v is [n_pages][n_kv_heads][head_dim][page_size])")
+        self.k, self.v, self.dtype = k, v, k.dtype
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = pages, page, heads, d
+        self.desc = SqKvCacheDesc(k.data_ptr(), v.data_ptr(), pages, page, heads, d, code)
+        self.ref = ctypes.byref(self.desc)
+
+
+def sq_block_tables(ctx_lens, new_lens, page_size: int, free_pages, block_table, seq_lens, cu_new,
+                    cu_pages, slot_map, result, stream=None) -> None:
+    """Extend the rows of block_table [n_req][stride] by the pages that new_lens
+    tokens after ctx_lens need (taken from free_pages in order) and write
+    seq_lens, cu_new, cu_pages, the slot of every new token and a result word."""
+    w, i32 = "sq_block_tables", (torch.int32,)
+    n = int(ctx_lens.numel())
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise SqError(SQ_ERR_INVALID, f"{w} (block_table is [n_req][stride])")
+    _arg(ctx_lens, w, "ctx_lens", i32, n)
+    _arg(new_lens, w, "new_lens", i32, n)
+    _arg(free_pages, w, "free_pages", i32, free_pages.numel())
+    _arg(block_table, w, "block_table", i32, block_table.numel())
+    _arg(seq_lens, w, "seq_lens", i32, n)
+    _arg(cu_new, w, "cu_new", i32, n + 1)
+    _arg(cu_pages, w, "cu_pages", i32, n + 1)
+    _arg(slot_map, w, "slot_map", (torch.int64,), slot_map.numel())
+    _arg(result, w, "result", i32, 1)
+    _check(_lib.sq_block_tables(_ptr(ctx_lens), _ptr(new_lens), n, int(page_size), _ptr(free_pages),
+                                free_pages.numel(), _ptr(block_table), block_table.shape[1],
+                                _ptr(seq_lens), _ptr(cu_new), _ptr(cu_pages), _ptr(slot_map),
+                                slot_map.numel(), _ptr(result), _stream(stream)), w)
+
+
+def sq_kv_append(cache: SqKvCache, k, v, slot_map, stream=None) -> None:
+    """cache[slot_map[t]] = k[t], v[t]; k, v [tokens][n_kv_heads][head_dim],
+    tokens may be strided; slots outside the cache are skipped."""
+    w, n = "sq_kv_append", int(slot_map.numel())
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    ks, vs = _rows(k, w, "k", cache.dtype, shape), _rows(v, w, "v", cache.dtype, shape)
+    _arg(slot_map, w, "slot_map", (torch.int64,), n)
+    _check(_lib.sq_kv_append(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs, slot_map.data_ptr(), n,
+                             _stream(stream)), w)
+
+
+def sq_paged_attention_workspace(cache: SqKvCache, n_req: int, n_heads: int, max_len: int) -> int:
+    return int(_lib.sq_paged_attention_workspace(cache.ref, n_req, n_heads, max_len))
+
+
+def sq_paged_attention(cache: SqKvCache, q, block_table, seq_lens, max_len: int, o, workspace=None,
+                       scale: float | None = None, window: int = 0, lse=None, stream=None) -> None:
+    """Attention of one new token per request, q [n_req][n_heads][head_dim], over
+    its cached tokens; scale defaults to head_dim ** -0.5, window 0 is no window.
+    `workspace`: sq_paged_attention_workspace bytes."""
+    w = "sq_paged_attention"
+    if q.dim() != 3:
+        raise SqError(SQ_ERR_INVALID, f"{w} (q is [n_req][n_heads][head_dim])")
+    n, heads, d = q.shape
+    qs = _rows(q, w, "q", cache.dtype, (n, heads, cache.head_dim))
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise SqError(SQ_ERR_INVALID, f"{w} (block_table is [n_req][stride])")
+    _arg(block_table, w, "block_table", (torch.int32,), block_table.numel())
+    _arg(seq_lens, w, "seq_lens", (torch.int32,), n)
+    _arg(o, w, "o", (cache.dtype,), n * heads * d)
+    _arg(lse, w, "lse", (torch.float32,), n * heads, optional=True)
+    ws, nb = _workspace(workspace, w)
+    _check(_lib.sq_paged_attention(cache.ref, q.data_ptr(), qs, n, heads, block_table.data_ptr(),
+                                   block_table.shape[1], seq_lens.data_ptr(), int(max_len),
+                                   d ** -0.5 if scale is None else float(scale), int(window),
+                                   o.data_ptr(), _ptr(lse), ws, nb, _stream(stream)), w)
