@@ -170,7 +170,8 @@ def test_large_and_small_values(sq, scale):
 def test_two_parts_make_the_whole(sq, dtype, rule):
     """Prompts given in two calls, the state handed on in place."""
     x = make(17, [133, 133], 3, 3, 128, 128, dtype)
-    o, S = run(sq, x, rule)
+    o, S = ref.prefill(x["q"].float(), x["k"].float(), x["v"].float(), x["alpha"], x["beta"], x["cu"], x["S0"],
+                       rule == 0)
     cuts, got, state = [0, 50, 133], np.zeros_like(o), x["S0"].cuda()
     cu = x["cu"]
     for lo, hi in zip(cuts, cuts[1:]):
@@ -223,17 +224,21 @@ def test_repeated_calls_are_bit_identical(sq):
         assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
 
 
-def test_sequences_do_not_touch_each_other(sq):
-    """NaN in one sequence stays in it."""
-    x = make(25, [70, 65, 3], 2, 2, 128, 128, "bf16")
-    clean = run(sq, x, 0)
-    x["v"][75] = float("nan")
-    o, S = run(sq, x, 0)
-    cu = x["cu"]
-    for s in (0, 2):
-        assert np.array_equal(o[cu[s]:cu[s + 1]], clean[0][cu[s]:cu[s + 1]])
-        assert np.array_equal(S[s], clean[1][s])
-    assert np.array_equal(o[70:75], clean[0][70:75]) and np.isnan(o[75:135]).all() and np.isnan(S[1]).all()
+def test_a_nan_stays_in_its_sequence(sq):
+    """NaN in one token leaves other sequences and earlier chunks of 64 tokens
+    alone and reaches every later token; token by token it is causal."""
+    for dtype in ("bf16", "f32"):
+        x = make(25, [70, 165, 3], 2, 2, 128, 128, dtype)
+        clean = run(sq, x, 0)
+        x["v"][145] = float("nan")
+        o, S = run(sq, x, 0)
+        cu = x["cu"]
+        for s in (0, 2):
+            assert np.array_equal(o[cu[s]:cu[s + 1]], clean[0][cu[s]:cu[s + 1]])
+            assert np.array_equal(S[s], clean[1][s])
+        same = 134 if dtype == "bf16" else 145
+        assert np.array_equal(o[70:same], clean[0][70:same])
+        assert np.isnan(o[145:235]).all() and np.isnan(S[1]).all()
 
 
 def test_offsets_outside_the_tokens_are_held(sq):
