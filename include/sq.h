@@ -286,9 +286,10 @@ uint64_t sq_prefill_workspace(int32_t n_seq, int32_t n_tokens, int32_t n_heads, 
  * outside [0, n_tokens] are held to that range, nothing outside the buffers
  * is touched, but tokens that it assigns to two sequences, or to none, have
  * undefined outputs.  bfloat16 with d_k = d_v = 128, strides in multiples of
- * 8 elements and 16-byte aligned q, k, v, o takes the chunked matrix kernels,
+ * 8 elements (at most 2^23), 16-byte aligned q, k, v, o and more than 12 tokens a
+ * sequence on average takes the chunked matrix kernel,
  * everything else a token-by-token one.  Non-finite inputs are a caller error:
- * they reach the outputs of their own sequence only, but in the chunked kernels
+ * they reach the outputs of their own sequence only, but in the chunked kernel
  * also those of earlier tokens of the same 64.  Errors: SQ_ERR_INVALID (null
  * or misaligned pointer, bad size, stride or enum, workspace too small),
  * SQ_ERR_UNSUPPORTED (d_k or d_v, or more tiles than one launch grid),

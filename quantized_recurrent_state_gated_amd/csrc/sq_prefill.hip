@@ -163,15 +163,16 @@ hipError_t tokens_t(const PrefillArgs &a, hipStream_t st)
 //
 // C = 64 tokens at a time.  With G_i the running sum of log2 alpha in the
 // chunk, D_ij = 2^(G_i - G_j) and S the state before it,
-//     W = T (V - 2^G (K S)),   T = (I + tril(beta_i D_ij k_i.k_j, -1))^-1 diag(beta)
+//     (I + tril(beta_i D_ij k_i.k_j, -1)) W = beta (V - 2^G (K S))
 //     O = 2^G (Q S) + tril(D_ij q_i.k_j) W
 //     S' = 2^G_C S + K^T (2^(G_C - G) W)
 // (plain decay: W = beta V).  Everything is a product of 64- and 128-wide
-// matrices, on the 16 x 16 x 32 bfloat16 matrix instructions.  T depends on
-// the keys and gates only: k_prefill_prepare makes it for all chunks at once;
-// k_prefill_chunks then walks a sequence chunk by chunk, a wave holding
-// 16 NT columns of the state in its accumulators (columns of S, V, W and O
-// go together and never meet others).
+// matrices, on the 16 x 16 x 32 bfloat16 matrix instructions.  The triangular
+// system is solved by halves of 32 tokens: T_a, T_b are the inverses of its
+// diagonal blocks (times beta), N the block D_ij k_i.k_j below, and
+//     W_a = T_a X_a,   W_b = T_b (X_b - N W_a),   X = V - 2^G (K S).
+// (Inverting all 64 rows at once costs four times the products of the two
+// halves, on the slow fp32 matrix instructions.)
 //
 // Precision.  q, k and v are bfloat16, exact operands.  What is fp32 (S, T, W)
 // enters a product as the sum of bfloat16 planes cut from its own mantissa:
@@ -181,12 +182,13 @@ hipError_t tokens_t(const PrefillArgs &a, hipStream_t st)
 // bfloat16, takes two.
 //
 // Operand order.  A 16 x 16 result holds rows 4 (lane / 16) + r of column
-// lane % 16; an operand wants, per lane, 8 of 32 consecutive indexes of the
-// summed axis.  Two results on top of each other are taken as that operand
-// directly by counting the axis in the order the results hold it: slot (g, i)
-// is index 4 g + i of the first for i < 4, of the second for i >= 4.  The
-// other operand is stored in shared memory in the same order ("fragments" of
-// 64 lanes x 16 bytes), so no product's result passes through memory.
+// lane % 16; an operand wants, per lane, 8 consecutive indexes 8 (lane / 16) + i
+// of the 32 that an instruction sums over.  So result m holds, for the axis it
+// shares with a later product, row x = index 32 (m / 2) + 8 (x / 4) + 4 (m % 2)
+// + x % 4 (perm below): results 2 n and 2 n + 1 are then together, in the
+// lane's own registers, the operand of indexes 32 n .. 32 n + 31.  No product's
+// result passes through memory.  O is made transposed (the same registers as
+// the other operand), so that a lane ends with four neighbouring columns.
 
 constexpr int kC = 64, kD = 128;
 
@@ -194,14 +196,19 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// 2^x for a difference of running sums (held in double: at half-lives of a
-// few tokens they reach hundreds, and their difference has to keep its last bits)
+__device__ __forceinline__ constexpr int perm(int m, int x)
+{
+    return 32 * (m >> 1) + 8 * (x >> 2) + 4 * (m & 1) + (x & 3);
+}
+
+// 2^x for running sums that may be long: the fraction is taken in double
 __device__ __forceinline__ float pow2(double x)
 {
     x = x < -160.0 ? -160.0 : x;
@@ -209,156 +216,8 @@ __device__ __forceinline__ float pow2(double x)
     return __builtin_ldexpf(__builtin_amdgcn_exp2f((float)(x - n)), (int)n);
 }
 
-// One record of the workspace per (chunk, head).
-struct Prep {
-    double G[kC];
-    float T[6][64][8];  // fragments of T's lower triangle, see frag_of
-};
-
-// Fragment f of a lower-triangular 64 x 64 operand: rows 16 mt .. + 15,
-// columns 32 ks .. + 31.  The order spreads the work of making them over the waves.
-__device__ __forceinline__ constexpr int frag_mt(int f) { return f == 0 || f == 1 ? 3 : f == 2 || f == 4 ? 2 : f == 3 ? 1 : 0; }
-__device__ __forceinline__ constexpr int frag_ks(int f) { return f == 1 || f == 4 ? 1 : 0; }
-__device__ __forceinline__ constexpr int frag_of(int mt, int ks)
-{
-    return mt == 3 ? ks : mt == 2 ? (ks ? 4 : 2) : mt == 1 ? 3 : 5;
-}
-
-// Chunk c of sequence s is record first / 64 + s + c: records of different
-// sequences are disjoint, and none reaches n_tokens / 64 + n_seq + 1.
-__host__ __device__ __forceinline__ int64_t prep_chunks(int32_t n_seq, int32_t n_tokens)
-{
-    return (int64_t)n_tokens / kC + n_seq + 1;
-}
-
-template <bool DELTA>
-__global__ __launch_bounds__(256) void k_prefill_prepare(PrefillArgs a)
-{
-    constexpr int LD = kC + 1;
-    __shared__ float M[DELTA ? kC * LD : 1], T[DELTA ? kC * LD : 1];
-    __shared__ double G[kC];
-    __shared__ float be[kC];
-    const int t = threadIdx.x, lane = t & 63, wv = t >> 6, g = lane >> 4, c = lane & 15;
-    const int h = (int)(blockIdx.x % (unsigned)a.heads);
-    const int64_t rec = blockIdx.x / (unsigned)a.heads;
-
-    // the sequence: the last s with cu[s] / 64 + s <= rec
-    int lo = 0, hi = a.n_seq;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((int64_t)(seq_of(a, mid).first / kC) + mid <= rec) lo = mid;
-        else hi = mid;
-    }
-    const Seq sr = seq_of(a, lo);
-    const int64_t t0 = sr.first + (rec - (sr.first / kC) - lo) * kC;
-    if (t0 < sr.first || t0 >= sr.last) return;
-    const int nt = sr.last - t0 < kC ? (int)(sr.last - t0) : kC;
-    Prep &out = reinterpret_cast<Prep *>(a.ws)[rec * a.heads + h];
-
-    if (wv == 0) {
-        // running sums of log2 alpha; a gate of zero counts as 2^-2000
-        const float al = lane < nt ? a.alpha[(t0 + lane) * a.heads + h] : 1.0f;
-        double x = al > 0.0f ? log2((double)al) : -2000.0;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double y = __shfl_up(x, d);
-            if (lane >= d) x += y;
-        }
-        out.G[lane] = x;
-        if (DELTA) {
-            G[lane] = x;
-            be[lane] = lane < nt ? a.beta[(t0 + lane) * a.heads + h] : 0.0f;
-        }
-    }
-    if constexpr (!DELTA) return;
-    // wave w: tiles (w, 0 .. w) of K K^T, straight from global memory
-    const uint16_t *k = reinterpret_cast<const uint16_t *>(a.k) + t0 * a.k_stride + (int64_t)(h / a.per_k) * kD;
-    bf16x8 ki[4];
-#pragma unroll
-    for (int s = 0; s < 4; s++) {
-        const int row = 16 * wv + c;
-        u32x4 x = {0, 0, 0, 0};
-        if (row < nt) x = *reinterpret_cast<const u32x4 *>(k + row * a.k_stride + 32 * s + 8 * g);
-        ki[s] = __builtin_bit_cast(bf16x8, x);
-    }
-    f32x4 kk[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        kk[j] = f32x4{0, 0, 0, 0};
-        if (j > wv) continue;
-#pragma unroll
-        for (int s = 0; s < 4; s++) {
-            const int row = 16 * j + c;
-            u32x4 x = {0, 0, 0, 0};
-            if (row < nt) x = *reinterpret_cast<const u32x4 *>(k + row * a.k_stride + 32 * s + 8 * g);
-            kk[j] = mma(ki[s], __builtin_bit_cast(bf16x8, x), kk[j]);
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        if (j > wv) continue;
-#pragma unroll
-        for (int r = 0; r < 4; r++) {
-            const int i = 16 * wv + 4 * g + r, jj = 16 * j + c;
-            M[i * LD + jj] = i > jj ? be[i] * pow2(G[i] - G[jj]) * kk[j][r] : 0.0f;
-        }
-    }
-    __syncthreads();
-    // wave w: inverse of its own 16 x 16 diagonal block, lane = column, by
-    // forward substitution
-    {
-        float x[16];
-        const int b = 16 * wv;
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-            float v = i == c ? 1.0f : 0.0f;
-#pragma unroll
-            for (int l = 0; l < i; l++) v = fmaf(-M[(b + i) * LD + b + l], x[l], v);
-            x[i] = v;
-        }
-        if (g == 0) {
-#pragma unroll
-            for (int i = 0; i < 16; i++) T[(b + i) * LD + b + c] = x[i];
-        }
-    }
-    __syncthreads();
-    // the blocks below, one diagonal after the other:
-    // T_ij = -T_ii sum_{l=j}^{i-1} M_il T_lj (fp32 matrix instructions)
-#pragma unroll
-    for (int d = 1; d < 4; d++) {
-        if (wv < 4 - d) {
-            const int j = wv, i = wv + d;
-            f32x4 R = {0, 0, 0, 0}, X = {0, 0, 0, 0};
-            for (int l = j; l < i; l++)
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    R = __builtin_amdgcn_mfma_f32_16x16x4f32(M[(16 * i + c) * LD + 16 * l + 4 * g + e],
-                                                             T[(16 * l + 4 * g + e) * LD + 16 * j + c], R, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                X = __builtin_amdgcn_mfma_f32_16x16x4f32(T[(16 * i + c) * LD + 16 * i + 4 * g + e], R[e], X, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; r++) T[(16 * i + 4 * g + r) * LD + 16 * j + c] = -X[r];
-        }
-        __syncthreads();
-    }
-    // fragments of T diag(beta)
-    for (int f = wv; f < 6; f += 4) {
-        const int mt = frag_mt(f), ks = frag_ks(f);
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int row = 16 * mt + c, col = 32 * ks + (i >> 2) * 16 + 4 * g + (i & 3);
-            v[i] = row >= col ? T[row * LD + col] * be[col] : 0.0f;
-        }
-        f32x4 *dst = reinterpret_cast<f32x4 *>(&out.T[f][lane][0]);
-        dst[0] = f32x4{v[0], v[1], v[2], v[3]};
-        dst[1] = f32x4{v[4], v[5], v[6], v[7]};
-    }
-}
-
-// The first NP planes of 8 fp32 values (two results a, b) as operands.
+// NP planes of 8 fp32 values as operands: each takes the top 16 bits of what
+// the planes before it left.
 template <int NP>
 __device__ __forceinline__ void planes(const f32x4 &a, const f32x4 &b, bf16x8 (&p)[NP])
 {
@@ -377,352 +236,679 @@ __device__ __forceinline__ void planes(const f32x4 &a, const f32x4 &b, bf16x8 (&
     }
 }
 
-constexpr int kFragBytes = 1024 + 16;  // 64 lanes x 16 bytes; the pad spreads transposed writes over the banks
+// Fragment f of a lower-triangular 64 x 64 operand: rows perm(mt, 0 .. 15),
+// columns 32 ks .. + 31 (ks <= mt / 2; the rest is zero).
+__device__ __forceinline__ constexpr int frag_of(int mt, int ks) { return mt + 2 * ks; }
 
+// Keys and queries lie in shared memory row by row, the 16-byte pieces of row
+// x exchanged by swz(x): the 16 rows that an operand's lanes read at once fall
+// on 16 different bank groups.  Transposed keys (for the state's update) are
+// read from the same rows by the transposing LDS read.
+__device__ __forceinline__ constexpr int swz(int x) { return ((x >> 3) & 3) << 2 | (x & 3); }
+
+constexpr int kH = 32, kLD = kH + 4;  // halves of the triangular system; rows stay 16-byte aligned
+
+struct Side {
+    double G[kC];                            // running sums of log2 alpha
+    float gam[kC], dec[kC], gf[kC], be[kC];  // 2^G, 2^(G_C - G), G, beta
+};
 struct SmemChunk {
-    alignas(16) unsigned char K[16 * kFragBytes];      // [mt 4][ks 4]: rows tokens, axis d_k
-    alignas(16) unsigned char Q[16 * kFragBytes];
-    alignas(16) unsigned char KT[16 * kFragBytes];     // [mt 8][ks 2]: rows d_k, axis tokens
-    alignas(16) unsigned char P[2][6 * kFragBytes];    // planes of tril(D q.k)
-    alignas(16) float gam[kC], dec[kC];                // 2^G, 2^(G_C - G)
-    alignas(16) double G[kC];
-    alignas(16) float be[kC];
+    alignas(16) unsigned char K[2][kC * 256];
+    alignas(16) unsigned char Q[2][kC * 256];
+    alignas(16) unsigned char P[2][2][6 * 1024];  // planes of tril(D q.k), fragments
+    alignas(16) Side side[3];
 };
-struct SmemChunkT : SmemChunk {
-    alignas(16) unsigned char T[3][6 * kFragBytes];    // planes of T
+struct SmemChunkDelta : SmemChunk {
+    alignas(16) unsigned char T[2][3][6 * 1024];  // planes of T_a, -N, T_b, fragments
+    alignas(16) float A[2][kH * kLD];             // scratch of the inversion
 };
 
-__device__ __forceinline__ bf16x8 frag(const unsigned char *base, int f, int lane)
+__device__ __forceinline__ bf16x8 lds16(const unsigned char *p)
 {
-    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(base + f * kFragBytes + lane * 16));
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(p));
 }
 
-template <bool DELTA, int NT, int NW>
-__global__ __launch_bounds__(64 * NW) void k_prefill_chunks(PrefillArgs a)
+// the shared-memory barrier alone: loads and stores in flight to global memory
+// (the next chunk's inputs, this chunk's outputs) are not waited for
+__device__ __forceinline__ void lds_barrier()
 {
-    constexpr int TH = 64 * NW, U = 256 / TH, COLS = 16 * NT * NW, NTV = 768 / TH;
-    using SM = typename std::conditional<DELTA, SmemChunkT, SmemChunk>::type;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// order of one wave's own shared-memory accesses across its lanes (the
+// hardware keeps it; this keeps the compiler to it)
+__device__ __forceinline__ void wave_order() { asm volatile("" ::: "memory"); }
+
+// Rows of global memory, `n` of `row` bytes, `stride` bytes apart: reads past
+// the last are zero, writes past it are dropped (the buffer instructions' own
+// range check), so a chunk that ends inside the 64 tokens takes the same
+// instructions as a whole one.  Offsets go into the lane's part: a scalar offset
+// is not covered by the check in every case.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void *p, int n, int32_t stride, int32_t row)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (n - 1) * stride + row, 0x00027000);
+}
+
+// x, in a way that keeps sums with it from being made ahead of a loop (they
+// would hold a register each through all of it)
+__device__ __forceinline__ int32_t here(int32_t x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// log2 of x > 0 to the last bits of an fp32 result, also next to 1 where the
+// result is small: exponent and log2 of the mantissa m in [0.7, 1.4) as
+// 2 / ln 2 (y + y^3 / 3 + ...), y = (m - 1) / (m + 1), |y| < 0.172.
+__device__ __forceinline__ double log2_exact(float x)
+{
+    int e;
+    float m = frexpf(x, &e);  // [0.5, 1)
+    if (m < 0.70710678f) {
+        m *= 2.0f;
+        e -= 1;
+    }
+    const float y = (m - 1.0f) / (m + 1.0f), z = y * y;
+    float p = 1.0f / 11.0f;
+    p = fmaf(p, z, 1.0f / 9.0f);
+    p = fmaf(p, z, 1.0f / 7.0f);
+    p = fmaf(p, z, 1.0f / 5.0f);
+    p = fmaf(p, z, 1.0f / 3.0f);
+    p = fmaf(p * z, y, y);
+    return (double)e + (double)p * 2.8853900817779268;
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double x)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, true);
+    return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Gates of one chunk, a lane per token.  The running sums are double: at
+// half-lives of a few tokens they reach hundreds, and their differences have to
+// keep their last bits.  A gate of zero counts as 2^-200: nothing before it is
+// left.
+__device__ __forceinline__ void make_side(Side &sd, int lane, float al, float bt)
+{
+    double x = al > 0.0f ? log2_exact(al) : al == 0.0f ? -200.0 : __builtin_nan("");
+    x = dpp_add<0x111, 0xf>(x);  // row_shr 1, 2, 4, 8: sums within 16 lanes
+    x = dpp_add<0x112, 0xf>(x);
+    x = dpp_add<0x114, 0xf>(x);
+    x = dpp_add<0x118, 0xf>(x);
+    x = dpp_add<0x142, 0xa>(x);  // last lane of a row into the next: rows 1 and 3
+    x = dpp_add<0x143, 0xc>(x);  // lane 31 into rows 2 and 3
+    const double last = __shfl(x, 63);
+    sd.G[lane] = x;
+    sd.gam[lane] = pow2(x);
+    sd.dec[lane] = pow2(last - x);
+    sd.gf[lane] = (float)x;
+    sd.be[lane] = bt;
+}
+
+// The products of one 16-row fragment: rows perm(mt, .) of q (or k) with the 32
+// keys of kf, transposed (a lane gets one row's 8 weights: the operand's order).
+struct Pair {
+    f32x4 p[2];
+};
+__device__ __forceinline__ Pair products(const bf16x8 (&kf)[2][4], const bf16x8 (&rf)[4])
+{
+    Pair y{{f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}};
+#pragma unroll
+    for (int x = 0; x < 4; x++)
+#pragma unroll
+        for (int u = 0; u < 2; u++) y.p[u] = mma(kf[u][x], rf[x], y.p[u]);
+    return y;
+}
+
+// A fragment of tril(D_ij q_i.k_j), two planes.
+__device__ __forceinline__ void put_P(unsigned char (&P)[2][6 * 1024], const Side &sd, int mt, int ks, Pair y, int lane,
+                                      int g, int c)
+{
+    const int i = perm(mt, c);
+    const float Gi = sd.gf[i];
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+        const int j0 = perm(2 * ks + u, 4 * g);
+        const f32x4 Gj = *reinterpret_cast<const f32x4 *>(&sd.gf[j0]);
+#pragma unroll
+        for (int r = 0; r < 4; r++) y.p[u][r] = j0 + r <= i ? y.p[u][r] * __builtin_amdgcn_exp2f(Gi - Gj[r]) : 0.0f;
+    }
+    bf16x8 pl[2];
+    planes<2>(y.p[0], y.p[1], pl);
+#pragma unroll
+    for (int n = 0; n < 2; n++)
+        *reinterpret_cast<u32x4 *>(P[n] + frag_of(mt, ks) * 1024 + lane * 16) = __builtin_bit_cast(u32x4, pl[n]);
+}
+
+// A fragment of -N (N_ij = D_ij k_i.k_j, i in the second half, j in the first),
+// three planes: it reaches the state, so D is taken from the double sums.
+__device__ __forceinline__ void put_N(unsigned char (&T)[3][6 * 1024], const Side &sd, int mt, Pair y, int lane, int g,
+                                      int c)
+{
+    const double Gi = sd.G[perm(mt, c)];
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int r = 0; r < 4; r++)
+            y.p[u][r] *= -__builtin_amdgcn_exp2f((float)(Gi - sd.G[perm(u, 4 * g) + r]));
+    bf16x8 pl[3];
+    planes<3>(y.p[0], y.p[1], pl);
+#pragma unroll
+    for (int n = 0; n < 3; n++)
+        *reinterpret_cast<u32x4 *>(T[n] + frag_of(mt, 0) * 1024 + lane * 16) = __builtin_bit_cast(u32x4, pl[n]);
+}
+
+// T_a and T_b of one chunk as three planes, by one wave.  kf[j][x]: keys
+// 16 j + c, d = 32 x + 8 g ...  The four 16 x 16 diagonal blocks are inverted at
+// once by forward substitution (a lane per column; stable whatever the keys,
+// where a product of powers of the matrix is not), the block below each pair is
+// -T_11 M_10 T_00 on the fp32 matrix instructions.
+struct Gram {
+    f32x4 kk[2][3];  // per half: blocks (0, 0), (1, 0), (1, 1) of K K^T
+};
+__device__ __forceinline__ Gram gram(const bf16x8 (&kf)[4][4])
+{
+    Gram y;
+#pragma unroll
+    for (int b = 0; b < 2; b++)
+#pragma unroll
+        for (int u = 0; u < 3; u++) y.kk[b][u] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int x = 0; x < 4; x++)
+#pragma unroll
+        for (int u = 0; u < 3; u++)
+#pragma unroll
+            for (int b = 0; b < 2; b++)
+                y.kk[b][u] = mma(kf[2 * b + (u > 0)][x], kf[2 * b + (u > 1)][x], y.kk[b][u]);
+    return y;
+}
+
+// x_i = [i == c] + sum_{l < i} m_l(lane i) x_l, i = I .. 15
+template <int I>
+__device__ __forceinline__ void forward(const float (&m)[16], float (&x)[16], int c)
+{
+    float v = I == c ? 1.0f : 0.0f, w = 0.0f;
+#pragma unroll
+    for (int l = 0; l < I; l++) {
+        const float b = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m[l]), 0x150 + I, 0xf, 0xf, true));
+        if (l & 1) w = fmaf(b, x[l], w);
+        else v = fmaf(b, x[l], v);
+    }
+    x[I] = v + w;
+    if constexpr (I < 15) forward<I + 1>(m, x, c);
+}
+
+__device__ __forceinline__ void make_T(unsigned char (&T)[3][6 * 1024], float (&A)[2][kH * kLD], const Side &sd, Gram y,
+                                       int lane, int g, int c)
+{
+#pragma unroll
+    for (int b = 0; b < 2; b++)
+#pragma unroll
+        for (int u = 0; u < 3; u++) {
+            const int i0 = 16 * (u > 0) + 4 * g, j = 16 * (u > 1) + c;
+            const double Gj = sd.G[32 * b + j];
+            const f32x4 bi = *reinterpret_cast<const f32x4 *>(&sd.be[32 * b + i0]);
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const float m = bi[r] * __builtin_amdgcn_exp2f((float)(sd.G[32 * b + i0 + r] - Gj)) * y.kk[b][u][r];
+                A[b][(i0 + r) * kLD + j] = i0 + r > j ? m : 0.0f;
+            }
+        }
+    wave_order();
+    {
+        // block g: lane c brings row c of the matrix and leaves with column c of the
+        // inverse; element (i, l) comes from lane i by a broadcast within the 16 lanes
+        float *Ab = A[g >> 1] + 16 * (g & 1) * (kLD + 1);
+        float m[16], x[16];
+#pragma unroll
+        for (int l = 0; l < 16; l += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(Ab + c * kLD + l);
+#pragma unroll
+            for (int e = 0; e < 4; e++) m[l + e] = -v[e];
+        }
+        forward<0>(m, x, c);
+        wave_order();
+#pragma unroll
+        for (int i = 0; i < 16; i++) Ab[i * kLD + c] = x[i];
+    }
+    wave_order();
+    {
+        f32x4 R[2], X[2];
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+            R[b] = X[b] = f32x4{0, 0, 0, 0};
+            const f32x4 m = *reinterpret_cast<const f32x4 *>(A[b] + (16 + c) * kLD + 4 * g);
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                R[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(m[e], A[b][(4 * g + e) * kLD + c], R[b], 0, 0, 0);
+        }
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+            const f32x4 ti = *reinterpret_cast<const f32x4 *>(A[b] + (16 + c) * kLD + 16 + 4 * g);
+#pragma unroll
+            for (int e = 0; e < 4; e++) X[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(ti[e], R[b][e], X[b], 0, 0, 0);
+        }
+        wave_order();
+#pragma unroll
+        for (int b = 0; b < 2; b++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) A[b][(16 + 4 * g + r) * kLD + c] = -X[b][r];
+    }
+    wave_order();
+#pragma unroll
+    for (int mt = 0; mt < 4; mt++) {
+        const int b = mt >> 1, row = perm(mt & 1, c), col = 8 * g;
+        f32x4 v[2];
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            v[u] = *reinterpret_cast<const f32x4 *>(A[b] + row * kLD + col + 4 * u);
+            const f32x4 bb = *reinterpret_cast<const f32x4 *>(&sd.be[32 * b + col + 4 * u]);
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[u][e] = row >= col + 4 * u + e ? v[u][e] * bb[e] : 0.0f;
+        }
+        bf16x8 pl[3];
+        planes<3>(v[0], v[1], pl);
+#pragma unroll
+        for (int p = 0; p < 3; p++)
+            *reinterpret_cast<u32x4 *>(T[p] + frag_of(mt, b) * 1024 + lane * 16) = __builtin_bit_cast(u32x4, pl[p]);
+    }
+}
+
+// The n-th longest of up to 64 sequences (in order of index where lengths are
+// equal; above 64 sequences, simply the n-th).
+__device__ __forceinline__ int nth_longest(const PrefillArgs &a, int n, int lane)
+{
+    if (a.n_seq > 64) return n;
+    int len = -1;
+    if (lane < a.n_seq) {
+        const Seq r = seq_of(a, lane);
+        len = r.last - r.first;
+    }
+    int rank = 0;
+    for (int i = 0; i < a.n_seq; i++) {
+        const int other = __builtin_amdgcn_readlane(len, i);
+        rank += other > len || (other == len && i < lane);
+    }
+    return __builtin_ctzll(__ballot(lane < a.n_seq && rank == n));
+}
+
+// A workgroup walks one (sequence, head, 16 NW columns) chunk by chunk.  NW
+// waves hold 16 columns of the state each and do nothing but chunk n; four more
+// run ahead of them and make what is the same for all columns: they bring keys
+// and queries to shared memory and compute the gates, P, T and N of the chunks
+// to come.  One barrier a chunk.  Inputs are read once, and no intermediate
+// leaves the CU.
+template <bool DELTA, int NW>
+__global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
+{
+    using SM = typename std::conditional<DELTA, SmemChunkDelta, SmemChunk>::type;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     SM &sm = *reinterpret_cast<SM *>(smem_raw);
 
-    const int t = threadIdx.x, lane = t & 63, wv = t >> 6, g = lane >> 4, c = lane & 15;
-    const unsigned sh = blockIdx.x % (unsigned)(a.n_seq * a.heads);
-    const int split = (int)(blockIdx.x / (unsigned)(a.n_seq * a.heads));
-    const int h = (int)(sh % (unsigned)a.heads), s = (int)(sh / (unsigned)a.heads);
+    const int t = threadIdx.x, lane = t & 63, g = lane >> 4, c = lane & 15;
+    const int wv = __builtin_amdgcn_readfirstlane(t >> 6);
+    // workgroups of long sequences first (the rest fills in behind them); the
+    // column splits of a head next to each other
+    const int split = (int)(blockIdx.x % (unsigned)(8 / NW));
+    const unsigned rest = blockIdx.x / (unsigned)(8 / NW);
+    const int h = (int)(rest % (unsigned)a.heads), s = nth_longest(a, (int)(rest / (unsigned)a.heads), lane);
+    const int64_t sh = (int64_t)s * a.heads + h;
     const Seq sr = seq_of(a, s);
-    const int col = split * COLS + wv * 16 * NT + NT * c;  // this lane's NT columns
-    const int64_t tile = (int64_t)sh * kD * kD;
+    const int chunks = (sr.last - sr.first + kC - 1) / kC;
+    // row strides in bytes (the host has checked that 64 rows are below 2^31)
+    const int32_t ks2 = (int32_t)a.k_stride * 2, qs2 = (int32_t)a.q_stride * 2, vs2 = (int32_t)a.v_stride * 2;
+    const int32_t os2 = a.heads * kD * 2;
+    const uint16_t *q = reinterpret_cast<const uint16_t *>(a.q) + (int64_t)(h / a.per_k) * kD;
+    const uint16_t *k = reinterpret_cast<const uint16_t *>(a.k) + (int64_t)(h / a.per_k) * kD;
 
-    // the state: rows 16 m + 4 g + r
-    f32x4 S[8][NT];
+    auto first_of = [&](int n) { return (int64_t)sr.first + (int64_t)n * kC; };
+    auto tokens_of = [&](int n) {
+        const int64_t left = sr.last - first_of(n);
+        return left < kC ? (int)left : kC;
+    };
+    auto key_window = [&](int n) { return rows_of(k + first_of(n) * a.k_stride, tokens_of(n), ks2, 256); };
+    auto query_window = [&](int n) { return rows_of(q + first_of(n) * a.q_stride, tokens_of(n), qs2, 256); };
+    const int32_t rho = 8 * (c >> 2) + (c & 3);  // perm(m, c) = perm(m, 0) + rho
+
+    if (wv >= NW) {
+        if (chunks == 0) return;
+        const int role = wv - NW;
+        // an operand's pieces straight from global memory: rows perm(m, c)
+        auto rows = [&](__amdgpu_buffer_rsrc_t w, int32_t st, int m, bf16x8 (&f)[4]) {
+            const int32_t b = here(rho * st + 16 * g) + perm(m, 0) * st;
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+                f[x] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(w, b + 64 * x, 0, 0));
+        };
+        // In step n the state's waves are at chunk n (or have not begun); chunk n + 1
+        // is made ready, and the gates of chunk n + 2.
+        if (role <= 1) {
+            // 0: keys, and N (plain decay: half of P); 1: queries, gates and (delta) half of P.
+            // The wave reads back, as operands, rows that it has written itself.
+            float al = 1.0f, bt = 0.0f;
+            constexpr int PROLE = DELTA ? 1 : 0;
+            auto gates = [&](int n) {
+                const bool in = lane < tokens_of(n);
+                const int64_t i = (first_of(n) + lane) * a.heads + h;
+                al = in ? a.alpha[i] : 1.0f;
+                bt = in ? a.beta[i] : 0.0f;
+            };
+            const int32_t st = role == 0 ? ks2 : qs2;
+            if (role == 1) gates(0);
+            // rows of the next chunk, loaded a step ahead (which also brings them to
+            // the L2 cache for the waves that load operands from global memory)
+            u32x4 x[16];
+            auto load_rows = [&](int n) {
+                const auto w = role == 0 ? key_window(n) : query_window(n);
+                const int32_t b = here(g * st + c * 16);
+#pragma unroll
+                for (int u = 0; u < 16; u++) x[u] = __builtin_amdgcn_raw_buffer_load_b128(w, b + 4 * u * st, 0, 0);
+            };
+            load_rows(0);
+            for (int n = -2; n < chunks; n++) {
+                lds_barrier();
+                if (n + 1 >= 0 && n + 1 < chunks) {
+                    const auto kw = key_window(n + 1), qw = query_window(n + 1);
+                    bf16x8 f[2][4];
+                    if (role == PROLE) {
+#pragma unroll
+                        for (int m = 0; m < 2; m++) {
+                            if (DELTA) rows(kw, ks2, m, f[m]);  // keys, for the queries' wave
+                            else rows(qw, qs2, m, f[m]);        // queries, for the keys' wave
+                        }
+                    }
+                    unsigned char *dst = role == 0 ? sm.K[(n + 1) & 1] : sm.Q[(n + 1) & 1];
+#pragma unroll
+                    for (int u = 0; u < 16; u++) {
+                        const int row = 4 * u + g;
+                        *reinterpret_cast<u32x4 *>(dst + row * 256 + ((c ^ swz(row)) * 16)) = x[u];
+                    }
+                    if (n + 2 < chunks) load_rows(n + 2);
+                    wave_order();
+                    const Side &sd = sm.side[(n + 1) % 3];
+                    auto own = [&](int m, bf16x8 (&o)[4]) {
+#pragma unroll
+                        for (int x = 0; x < 4; x++)
+                            o[x] = lds16(dst + (perm(m, 0) + rho) * 256 + (((4 * x + g) ^ c) * 16));
+                    };
+                    if (role == PROLE && DELTA) {
+#pragma unroll
+                        for (int m = 0; m < 2; m++) {
+                            bf16x8 e[4];
+                            own(m, e);
+                            put_P(sm.P[(n + 1) & 1], sd, m, 0, products(f, e), lane, g, c);
+                        }
+                    } else if (role == PROLE) {
+                        bf16x8 e[2][4];
+                        own(0, e[0]);
+                        own(1, e[1]);
+#pragma unroll
+                        for (int m = 0; m < 2; m++) put_P(sm.P[(n + 1) & 1], sd, m, 0, products(e, f[m]), lane, g, c);
+                    } else if constexpr (DELTA) {
+                        bf16x8 e[2][4], i[4];
+                        own(0, e[0]);
+                        own(1, e[1]);
+#pragma unroll
+                        for (int m = 2; m < 4; m++) {
+                            own(m, i);
+                            put_N(sm.T[(n + 1) & 1], sd, m, products(e, i), lane, g, c);
+                        }
+                    }
+                }
+                if (role == 1 && n + 2 < chunks) {
+                    make_side(sm.side[(n + 2) % 3], lane, al, bt);
+                    if (n + 3 < chunks) gates(n + 3);
+                }
+            }
+        } else if (!DELTA || role == 2) {
+            // P's other half (plain decay: shared with the fourth wave)
+            constexpr int N = DELTA ? 2 : 1;
+            bf16x8 kf[N][2][4], qf[2][4];
+            const int ks0 = DELTA ? 0 : role - 2;
+            for (int n = -2; n < chunks; n++) {
+                lds_barrier();
+                if (n + 1 < 0 || n + 1 >= chunks) continue;
+                const auto kw = key_window(n + 1), qw = query_window(n + 1);
+#pragma unroll
+                for (int m = 0; m < 2; m++) {
+                    rows(qw, qs2, 2 + m, qf[m]);
+#pragma unroll
+                    for (int z = 0; z < N; z++) rows(kw, ks2, 2 * (ks0 + z) + m, kf[z][m]);
+                }
+#pragma unroll
+                for (int z = 0; z < N; z++)
+#pragma unroll
+                    for (int m = 0; m < 2; m++)
+                        put_P(sm.P[(n + 1) & 1], sm.side[(n + 1) % 3], 2 + m, ks0 + z, products(kf[z], qf[m]), lane, g, c);
+            }
+        } else if constexpr (DELTA) {
+            // T takes longest: its keys are loaded a step ahead, and it goes first
+            __builtin_amdgcn_s_setprio(2);
+            bf16x8 kf[4][4];
+            for (int n = -2; n < chunks; n++) {
+                lds_barrier();
+                const bool now = n + 1 >= 0 && n + 1 < chunks;
+                Gram y;
+                if (now) y = gram(kf);
+                if (n + 2 < chunks) {
+                    const auto kw = key_window(n + 2);
+                    const int32_t b = here(c * ks2 + 16 * g);
+#pragma unroll
+                    for (int m = 0; m < 4; m++)
+#pragma unroll
+                        for (int x = 0; x < 4; x++)
+                            kf[m][x] = __builtin_bit_cast(
+                                bf16x8, __builtin_amdgcn_raw_buffer_load_b128(kw, b + 16 * m * ks2 + 64 * x, 0, 0));
+                }
+                if (now) make_T(sm.T[(n + 1) & 1], sm.A, sm.side[(n + 1) % 3], y, lane, g, c);
+            }
+        }
+        return;
+    }
+
+    // the state: result m, row perm(m, 4 g + r), column col0 + c
+    const int col0 = (split * NW + wv) * 16;
+    const int64_t tile = sh * kD * kD + col0 + c;
+    f32x4 S[8];
 #pragma unroll
     for (int m = 0; m < 8; m++)
 #pragma unroll
-        for (int r = 0; r < 4; r++)
-#pragma unroll
-            for (int n = 0; n < NT; n++)
-                S[m][n][r] = a.S0 ? a.S0[tile + (int64_t)(16 * m + 4 * g + r) * kD + col + n] : 0.0f;
+        for (int r = 0; r < 4; r++) S[m][r] = a.S0 ? a.S0[tile + (int64_t)perm(m, 4 * g + r) * kD] : 0.0f;
 
-    const uint16_t *q = reinterpret_cast<const uint16_t *>(a.q) + (int64_t)(h / a.per_k) * kD;
-    const uint16_t *k = reinterpret_cast<const uint16_t *>(a.k) + (int64_t)(h / a.per_k) * kD;
-    const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v) + (int64_t)h * kD + col;
-    uint16_t *o = reinterpret_cast<uint16_t *>(a.o) + (int64_t)h * kD + col;
-    const Prep *prep = reinterpret_cast<const Prep *>(a.ws);
-    const int64_t rec0 = sr.first / kC + s, recs = prep_chunks(a.n_seq, a.n_tokens);
-
-    // one chunk's inputs, loaded a chunk ahead: unit u of a thread is tokens
-    // 4 tg .. + 3 and d = 8 dg .. + 7
-    u32x4 kr[U][4], qr[U][4];
-    f32x4 tr[DELTA ? NTV : 1];
-    uint32_t vr[4][4];
-    double Gr = 0.0, Gc = 0.0;
-    float br = 0.0f;
-    auto load = [&](int32_t t0) {
-        const int nt = sr.last - t0 < kC ? sr.last - t0 : kC;
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int id = t + TH * u, dg = id & 15, tg = id >> 4;
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int64_t tok = t0 + 4 * tg + r;
-                kr[u][r] = qr[u][r] = u32x4{0, 0, 0, 0};
-                if (4 * tg + r < nt) {
-                    kr[u][r] = *reinterpret_cast<const u32x4 *>(k + tok * a.k_stride + 8 * dg);
-                    qr[u][r] = *reinterpret_cast<const u32x4 *>(q + tok * a.q_stride + 8 * dg);
-                }
-            }
-        }
-        int64_t rec = rec0 + (t0 - sr.first) / kC;
-        rec = (rec < recs ? rec : recs - 1) * a.heads + h;
-        if constexpr (DELTA) {
-            const f32x4 *src = reinterpret_cast<const f32x4 *>(&prep[rec].T[0][0][0]);
-#pragma unroll
-            for (int i = 0; i < NTV; i++) tr[i] = src[t + TH * i];
-        }
-        if (t < kC) {
-            Gr = prep[rec].G[t];
-            Gc = prep[rec].G[kC - 1];
-            br = t < nt ? a.beta[(int64_t)(t0 + t) * a.heads + h] : 0.0f;
-        }
+    const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v) + (int64_t)h * kD + col0;
+    uint16_t *o = reinterpret_cast<uint16_t *>(a.o) + (int64_t)h * kD + col0;
+    const int32_t at_v = 8 * g * vs2 + 2 * c, at_o = rho * os2 + 8 * g;
+    uint16_t vr[4][4];  // the next chunk's values
+    auto load_v = [&](int n) {
+        const auto w = rows_of(v + first_of(n) * a.v_stride, tokens_of(n), vs2, 32);
+        const int32_t b = here(at_v);
 #pragma unroll
         for (int m = 0; m < 4; m++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int x = 16 * m + 4 * g + r;
-                vr[m][r] = 0;
-                if (x < nt) {
-                    const uint16_t *p = v + (int64_t)(t0 + x) * a.v_stride;
-                    if constexpr (NT == 2) vr[m][r] = *reinterpret_cast<const uint32_t *>(p);
-                    else vr[m][r] = *p;
+            for (int r = 0; r < 4; r++)
+                vr[m][r] = __builtin_amdgcn_raw_buffer_load_b16(w, b + perm(m, r) * vs2, 0, 0);
+    };
+    // swz(perm(m, c)) = c: piece 4 x + g of row perm(m, c) lies here, perm(m, 0) rows on
+    int at_row[4], at_kt[4];
+#pragma unroll
+    for (int x = 0; x < 4; x++) {
+        at_row[x] = rho * 256 + (((4 * x + g) ^ c) * 16);
+        // transposing read: lanes 4 i + z of 16 read token 8 g + i (+ 32 ks + 4 u, which
+        // leaves swz alone), d 32 x + 8 z (+ 4); each gets four tokens of one d
+        at_kt[x] = (8 * g + (c >> 2)) * 256 + (((4 * x + (c & 3)) ^ swz(8 * g + (c >> 2))) * 16);
+    }
+    auto rows = [&](const unsigned char *base, int m, int x) { return lds16(base + at_row[x] + perm(m, 0) * 256); };
+
+    if (chunks > 0) {
+        load_v(0);
+        lds_barrier();
+        lds_barrier();
+    }
+    for (int n = 0; n < chunks; n++) {
+        lds_barrier();
+        const unsigned char *K = sm.K[n & 1], *Q = sm.Q[n & 1];
+        const Side &sd = sm.side[n % 3];
+        f32x4 W[4];  // V, then V - 2^G K S, then W
+#pragma unroll
+        for (int m = 0; m < 4; m++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) W[m][r] = __uint_as_float((uint32_t)vr[m][r] << 16);
+        if (n + 1 < chunks) load_v(n + 1);
+
+        // K S, and S^T Q^T
+        f32x4 O[4];
+        {
+            f32x4 KS[4];
+#pragma unroll
+            for (int m = 0; m < 4; m++) O[m] = KS[m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+                bf16x8 sp[3];
+                planes<3>(S[2 * x], S[2 * x + 1], sp);
+#pragma unroll
+                for (int mh = 0; mh < 4; mh += 2) {
+                    bf16x8 qf[2], kf[2];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        qf[i] = rows(Q, mh + i, x);
+                        if constexpr (DELTA) kf[i] = rows(K, mh + i, x);
+                    }
+#pragma unroll
+                    for (int p = 0; p < 3; p++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            if (p < 2) O[mh + i] = mma(sp[p], qf[i], O[mh + i]);
+                            if constexpr (DELTA) KS[mh + i] = mma(kf[i], sp[p], KS[mh + i]);
+                        }
                 }
             }
-    };
-
-    if (sr.first < sr.last) load(sr.first);
-    for (int32_t t0 = sr.first; t0 < sr.last; t0 += kC) {
-        // registers -> fragments in shared memory
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int id = t + TH * u, dg = id & 15, tg = id >> 4;
-            const int ks = dg >> 2, half = (dg >> 1) & 1, g0 = (dg & 1) * 2;
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int x = 4 * tg + r;
-                const int at = ((x >> 4) * 4 + ks) * kFragBytes + (g0 * 16 + (x & 15)) * 16 + half * 8;
-                *reinterpret_cast<u32x2 *>(sm.K + at) = u32x2{kr[u][r][0], kr[u][r][1]};
-                *reinterpret_cast<u32x2 *>(sm.K + at + 256) = u32x2{kr[u][r][2], kr[u][r][3]};
-                *reinterpret_cast<u32x2 *>(sm.Q + at) = u32x2{qr[u][r][0], qr[u][r][1]};
-                *reinterpret_cast<u32x2 *>(sm.Q + at + 256) = u32x2{qr[u][r][2], qr[u][r][3]};
-            }
-            const int tk = tg >> 3, tgg = tg & 3, th = (tg >> 2) & 1;
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const int d = 8 * dg + e;
-                const uint32_t sel = (e & 1) ? 0x07060302u : 0x05040100u;
-                const uint32_t lo = __builtin_amdgcn_perm(kr[u][1][e >> 1], kr[u][0][e >> 1], sel);
-                const uint32_t hi = __builtin_amdgcn_perm(kr[u][3][e >> 1], kr[u][2][e >> 1], sel);
-                *reinterpret_cast<u32x2 *>(sm.KT + ((d >> 4) * 2 + tk) * kFragBytes + (tgg * 16 + (d & 15)) * 16 +
-                                           th * 8) = u32x2{lo, hi};
+            for (int m = 0; m < 4; m++) {
+                O[m] *= sd.gam[perm(m, c)];
+                if constexpr (DELTA) W[m] -= *reinterpret_cast<const f32x4 *>(&sd.gam[perm(m, 4 * g)]) * KS[m];
+                else W[m] *= *reinterpret_cast<const f32x4 *>(&sd.be[perm(m, 4 * g)]);
             }
         }
-        if constexpr (DELTA) {
+        const float gC = sd.gam[kC - 1];
 #pragma unroll
-            for (int i = 0; i < NTV; i++) {
-                // four values: half a lane's 16 bytes of each plane
-                const int id = t + TH * i;
-                float x[4] = {tr[i][0], tr[i][1], tr[i][2], tr[i][3]};
+        for (int m = 0; m < 8; m++) S[m] *= gC;
+#pragma unroll
+        for (int ks = 0; ks < 2; ks++) {
+            const int m0 = 2 * ks;
+            bf16x8 wp[3];
+            if constexpr (DELTA) {
+                // W = T X, half by half; the first half's W then leaves X of the second
+                const auto &T = sm.T[n & 1];
+                planes<3>(W[m0], W[m0 + 1], wp);
+                f32x4 Y[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
                 for (int p = 0; p < 3; p++) {
-                    u32x2 w;
-                    w[0] = __builtin_amdgcn_perm(__float_as_uint(x[1]), __float_as_uint(x[0]), 0x07060302u);
-                    w[1] = __builtin_amdgcn_perm(__float_as_uint(x[3]), __float_as_uint(x[2]), 0x07060302u);
-                    *reinterpret_cast<u32x2 *>(sm.T[p] + (id >> 7) * kFragBytes + (id & 127) * 8) = w;
+                    const bf16x8 t0 = lds16(T[p] + frag_of(m0, ks) * 1024 + lane * 16);
+                    const bf16x8 t1 = lds16(T[p] + frag_of(m0 + 1, ks) * 1024 + lane * 16);
 #pragma unroll
-                    for (int e = 0; e < 4; e++) x[e] -= __uint_as_float(__float_as_uint(x[e]) & 0xffff0000u);
+                    for (int z = 0; z < 3 - p; z++) {
+                        Y[0] = mma(t0, wp[z], Y[0]);
+                        Y[1] = mma(t1, wp[z], Y[1]);
+                    }
                 }
-            }
-        }
-        if (t < kC) {
-            sm.G[t] = Gr;
-            sm.gam[t] = pow2(Gr);
-            sm.dec[t] = pow2(Gc - Gr);
-            sm.be[t] = br;
-        }
-        f32x4 X[4][NT];  // V, then V - 2^G K S
+                W[m0] = Y[0];
+                W[m0 + 1] = Y[1];
+                planes<3>(W[m0], W[m0 + 1], wp);
+                if (ks == 0) {
 #pragma unroll
-        for (int m = 0; m < 4; m++)
+                    for (int p = 0; p < 3; p++) {
+                        const bf16x8 t0 = lds16(T[p] + frag_of(2, 0) * 1024 + lane * 16);
+                        const bf16x8 t1 = lds16(T[p] + frag_of(3, 0) * 1024 + lane * 16);
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                X[m][0][r] = __uint_as_float(vr[m][r] << 16);
-                if constexpr (NT == 2) X[m][1][r] = __uint_as_float(vr[m][r] & 0xffff0000u);
-            }
-        __syncthreads();
-        const int nt = sr.last - t0 < kC ? sr.last - t0 : kC;
-        if (t0 + kC < sr.last) load(t0 + kC);
-
-        // tril(D_ij q_i.k_j), two planes: the transposed products K Q^T leave
-        // a lane one query's weights, which is the operand's order
-        for (int f = wv; f < 6; f += NW) {
-            const int mt = frag_mt(f), ks = frag_ks(f);
-            f32x4 p[2];
-            const double Gi = sm.G[16 * mt + c];
-#pragma unroll
-            for (int b = 0; b < 2; b++) {
-                const int jt = 2 * ks + b;
-                p[b] = f32x4{0, 0, 0, 0};
-                if (jt > mt) continue;
-#pragma unroll
-                for (int x = 0; x < 4; x++) p[b] = mma(frag(sm.K, jt * 4 + x, lane), frag(sm.Q, mt * 4 + x, lane), p[b]);
-#pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const int j = 16 * jt + 4 * g + r;
-                    p[b][r] = j <= 16 * mt + c ? p[b][r] * pow2(Gi - sm.G[j]) : 0.0f;
+                        for (int z = 0; z < 3 - p; z++) {
+                            W[2] = mma(t0, wp[z], W[2]);
+                            W[3] = mma(t1, wp[z], W[3]);
+                        }
+                    }
                 }
+            } else {
+                planes<3>(W[m0], W[m0 + 1], wp);
             }
-            bf16x8 pl[2];
-            planes<2>(p[0], p[1], pl);
+            // O^T = 2^G (S^T Q^T) + W^T P^T
+            bf16x8 p0[4], p1[4];
 #pragma unroll
-            for (int n = 0; n < 2; n++)
-                *reinterpret_cast<u32x4 *>(sm.P[n] + f * kFragBytes + lane * 16) = __builtin_bit_cast(u32x4, pl[n]);
-        }
-
-        // K S and Q S
-        f32x4 O[4][NT], KS[4][NT];
+            for (int m = m0; m < 4; m++) {
+                p0[m] = lds16(sm.P[n & 1][0] + frag_of(m, ks) * 1024 + lane * 16);
+                p1[m] = lds16(sm.P[n & 1][1] + frag_of(m, ks) * 1024 + lane * 16);
+            }
 #pragma unroll
-        for (int m = 0; m < 4; m++)
+            for (int m = m0; m < 4; m++) O[m] = mma(wp[0], p0[m], O[m]);
 #pragma unroll
-            for (int n = 0; n < NT; n++) O[m][n] = KS[m][n] = f32x4{0, 0, 0, 0};
+            for (int m = m0; m < 4; m++) O[m] = mma(wp[1], p0[m], O[m]);
 #pragma unroll
-        for (int x = 0; x < 4; x++) {
-            bf16x8 sp[NT][3];
+            for (int m = m0; m < 4; m++) O[m] = mma(wp[0], p1[m], O[m]);
+            // S' = 2^G_C S + K^T (2^(G_C - G) W)
+            const f32x4 d0 = *reinterpret_cast<const f32x4 *>(&sd.dec[32 * ks + 8 * g]);
+            const f32x4 d1 = *reinterpret_cast<const f32x4 *>(&sd.dec[32 * ks + 8 * g + 4]);
+            planes<3>(W[m0] * d0, W[m0 + 1] * d1, wp);
 #pragma unroll
-            for (int n = 0; n < NT; n++) planes<3>(S[2 * x][n], S[2 * x + 1][n], sp[n]);
+            for (int mh = 0; mh < 8; mh += 4) {
+                bf16x8 kt[4];
 #pragma unroll
-            for (int m = 0; m < 4; m++) {
-                const bf16x8 qf = frag(sm.Q, m * 4 + x, lane);
+                for (int i = 0; i < 4; i++) {
+                    const int m = mh + i;
+                    s16x4 part[2];
 #pragma unroll
-                for (int p = 0; p < 2; p++)
-#pragma unroll
-                    for (int n = 0; n < NT; n++) O[m][n] = mma(qf, sp[n][p], O[m][n]);
-                if constexpr (DELTA) {
-                    const bf16x8 kf = frag(sm.K, m * 4 + x, lane);
-#pragma unroll
-                    for (int p = 0; p < 3; p++)
-#pragma unroll
-                        for (int n = 0; n < NT; n++) KS[m][n] = mma(kf, sp[n][p], KS[m][n]);
+                    for (int u = 0; u < 2; u++)
+                        part[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (__attribute__((address_space(3))) s16x4 *)(K + at_kt[m >> 1] + (32 * ks + 4 * u) * 256 +
+                                                                       (m & 1) * 8));
+                    kt[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7));
                 }
-            }
-        }
-        // W
-        f32x4 W[4][NT];
-        if constexpr (DELTA) {
-#pragma unroll
-            for (int m = 0; m < 4; m++) {
-                const f32x4 gm = *reinterpret_cast<const f32x4 *>(&sm.gam[16 * m + 4 * g]);
-#pragma unroll
-                for (int n = 0; n < NT; n++) {
-                    O[m][n] *= gm;
-                    X[m][n] -= gm * KS[m][n];
-                    W[m][n] = f32x4{0, 0, 0, 0};
-                }
-            }
-#pragma unroll
-            for (int ks = 0; ks < 2; ks++) {
-                bf16x8 xp[NT][3];
-#pragma unroll
-                for (int n = 0; n < NT; n++) planes<3>(X[2 * ks][n], X[2 * ks + 1][n], xp[n]);
-#pragma unroll
-                for (int m = 2 * ks; m < 4; m++) {
-                    const int f = frag_of(m, ks);
-                    bf16x8 tf[3];
-#pragma unroll
-                    for (int p = 0; p < 3; p++) tf[p] = frag(sm.T[p], f, lane);
-#pragma unroll
-                    for (int p = 0; p < 3; p++)
-#pragma unroll
-                        for (int y = 0; y < 3 - p; y++)
-#pragma unroll
-                            for (int n = 0; n < NT; n++) W[m][n] = mma(tf[p], xp[n][y], W[m][n]);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int m = 0; m < 4; m++) {
-                const f32x4 gm = *reinterpret_cast<const f32x4 *>(&sm.gam[16 * m + 4 * g]);
-                const f32x4 bm = *reinterpret_cast<const f32x4 *>(&sm.be[16 * m + 4 * g]);
-#pragma unroll
-                for (int n = 0; n < NT; n++) {
-                    O[m][n] *= gm;
-                    W[m][n] = X[m][n] * bm;
-                }
-            }
-        }
-        __syncthreads();  // P is whole
-#pragma unroll
-        for (int ks = 0; ks < 2; ks++) {
-            bf16x8 wp[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; n++) planes<2>(W[2 * ks][n], W[2 * ks + 1][n], wp[n]);
-#pragma unroll
-            for (int m = 2 * ks; m < 4; m++) {
-                const int f = frag_of(m, ks);
-                const bf16x8 p0 = frag(sm.P[0], f, lane), p1 = frag(sm.P[1], f, lane);
-#pragma unroll
-                for (int n = 0; n < NT; n++) {
-                    O[m][n] = mma(p0, wp[n][0], O[m][n]);
-                    O[m][n] = mma(p0, wp[n][1], O[m][n]);
-                    O[m][n] = mma(p1, wp[n][0], O[m][n]);
-                }
-            }
-        }
-        // S' = 2^G_C S + K^T (2^(G_C - G) W)
-        const float gC = sm.gam[kC - 1];
-#pragma unroll
-        for (int m = 0; m < 8; m++)
-#pragma unroll
-            for (int n = 0; n < NT; n++) S[m][n] *= gC;
-#pragma unroll
-        for (int ks = 0; ks < 2; ks++) {
-            const f32x4 d0 = *reinterpret_cast<const f32x4 *>(&sm.dec[32 * ks + 4 * g]);
-            const f32x4 d1 = *reinterpret_cast<const f32x4 *>(&sm.dec[32 * ks + 16 + 4 * g]);
-            bf16x8 wp[NT][3];
-#pragma unroll
-            for (int n = 0; n < NT; n++) planes<3>(W[2 * ks][n] * d0, W[2 * ks + 1][n] * d1, wp[n]);
-#pragma unroll
-            for (int m = 0; m < 8; m++) {
-                const bf16x8 kf = frag(sm.KT, m * 2 + ks, lane);
 #pragma unroll
                 for (int p = 0; p < 3; p++)
 #pragma unroll
-                    for (int n = 0; n < NT; n++) S[m][n] = mma(kf, wp[n][p], S[m][n]);
+                    for (int i = 0; i < 4; i++) S[mh + i] = mma(kt[i], wp[p], S[mh + i]);
             }
         }
+        // a lane's four neighbouring columns of token perm(m, c)
+        const auto ow = rows_of(o + first_of(n) * a.heads * kD, tokens_of(n), os2, 32);
 #pragma unroll
-        for (int m = 0; m < 4; m++)
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int x = 16 * m + 4 * g + r;
-                if (x >= nt) continue;
-                uint16_t *p = o + (int64_t)(t0 + x) * a.heads * kD;
-                if constexpr (NT == 2)
-                    *reinterpret_cast<uint32_t *>(p) =
-                        (uint32_t)down<uint16_t>(O[m][0][r]) | ((uint32_t)down<uint16_t>(O[m][1][r]) << 16);
-                else
-                    *p = down<uint16_t>(O[m][0][r]);
-            }
-        __syncthreads();
+        for (int m = 0; m < 4; m++) {
+            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, __builtin_convertvector(O[m], bf16x4)),
+                                                  ow, here(at_o) + perm(m, 0) * os2, 0, 0);
+        }
     }
     if (!a.S) return;
 #pragma unroll
     for (int m = 0; m < 8; m++)
 #pragma unroll
-        for (int r = 0; r < 4; r++)
-#pragma unroll
-            for (int n = 0; n < NT; n++) a.S[tile + (int64_t)(16 * m + 4 * g + r) * kD + col + n] = S[m][n][r];
+        for (int r = 0; r < 4; r++) a.S[tile + (int64_t)perm(m, 4 * g + r) * kD] = S[m][r];
 }
 
-template <bool DELTA, int NT, int NW>
+template <bool DELTA, int NW>
 hipError_t chunks_t(const PrefillArgs &a, hipStream_t st)
 {
-    const unsigned grid = (unsigned)((int64_t)a.n_seq * a.heads * (kD / (16 * NT * NW)));
-    const size_t lds = DELTA ? sizeof(SmemChunkT) : sizeof(SmemChunk);
-    auto kern = k_prefill_chunks<DELTA, NT, NW>;
+    const unsigned grid = (unsigned)((int64_t)a.n_seq * a.heads * (8 / NW));
+    const size_t lds = DELTA ? sizeof(SmemChunkDelta) : sizeof(SmemChunk);
+    auto kern = k_prefill_chunks<DELTA, NW>;
     if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
         return e;
-    hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * NW), lds, st, a);
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * (NW + 4)), lds, st, a);
     return hipGetLastError();
 }
 
 template <bool DELTA>
 hipError_t chunked(const PrefillArgs &a, hipStream_t st)
 {
-    const int64_t blocks = prep_chunks(a.n_seq, a.n_tokens) * a.heads;
-    hipLaunchKernelGGL((k_prefill_prepare<DELTA>), dim3((unsigned)blocks), dim3(DELTA ? 256 : 64), 0, st, a);
-    if (hipError_t e = hipGetLastError()) return e;
-    const int64_t sh = (int64_t)a.n_seq * a.heads;
-    if (sh >= 192) return chunks_t<DELTA, 2, 4>(a, st);
-    return chunks_t<DELTA, 1, 2>(a, st);
+    // One workgroup fits a CU.  While the halves of all heads fit the 256 CUs
+    // together, two workgroups a head are faster (a step of fewer columns: delta,
+    // 96 heads x 4,096 tokens 310 us against 421, 48 heads 290 against 374; quarters
+    // 578 and 298); above that, whole heads, whose common work is done once
+    // (144 heads 431 us against 599, 192 heads 453 against 609).
+    return (int64_t)a.n_seq * a.heads <= 128 ? chunks_t<DELTA, 4>(a, st) : chunks_t<DELTA, 8>(a, st);
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
@@ -732,22 +918,22 @@ bool chunk_shape(int32_t dk, int32_t dv, bool bf16) { return bf16 && dk == kD &&
 
 bool chunk_aligned(const PrefillArgs &a)
 {
+    constexpr int64_t kMost = 1 << 23;  // elements between tokens: 64 rows stay below 2^31 bytes
     return aligned16(a.q) && aligned16(a.k) && aligned16(a.v) && aligned16(a.o) && a.q_stride % 8 == 0 &&
-           a.k_stride % 8 == 0 && a.v_stride % 8 == 0;
+           a.k_stride % 8 == 0 && a.v_stride % 8 == 0 && a.q_stride <= kMost && a.k_stride <= kMost &&
+           a.v_stride <= kMost && (int64_t)a.heads * kD <= kMost;
 }
 
 }  // namespace
 
-uint64_t prefill_workspace(int32_t n_seq, int32_t n_tokens, int32_t heads, int32_t dk, int32_t dv, bool bf16,
-                           bool)
-{
-    if (!chunk_shape(dk, dv, bf16)) return 0;
-    return (uint64_t)prep_chunks(n_seq, n_tokens) * (uint64_t)heads * sizeof(Prep);
-}
+uint64_t prefill_workspace(int32_t, int32_t, int32_t, int32_t, int32_t, bool, bool) { return 0; }
 
 hipError_t launch_prefill(const PrefillArgs &a, bool bf16, bool delta, hipStream_t st)
 {
-    if (chunk_shape(a.dk, a.dv, bf16) && chunk_aligned(a)) return delta ? chunked<true>(a, st) : chunked<false>(a, st);
+    // A few tokens a sequence go faster one by one than as a padded chunk (768 heads,
+    // 8 tokens each: 33 us against 42; 16 tokens 49 against 43).
+    const bool few = a.n_tokens <= 12 * (int64_t)a.n_seq;
+    if (chunk_shape(a.dk, a.dv, bf16) && chunk_aligned(a) && !few) return delta ? chunked<true>(a, st) : chunked<false>(a, st);
     if (bf16) return delta ? tokens_t<uint16_t, true>(a, st) : tokens_t<uint16_t, false>(a, st);
     return delta ? tokens_t<float, true>(a, st) : tokens_t<float, false>(a, st);
 }

@@ -123,9 +123,22 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_gpu_seen = False  # torch.cuda.is_available() asks the runtime anew on every call
+# the current stream's handle without a Stream object around it (torch has no
+# public name for this; without it the public call is used)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int | None:
+    global _gpu_seen
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        if _gpu_seen and _raw_stream is not None and _device is not None:
+            return _raw_stream(_device())
+        if not torch.cuda.is_available():
+            return None
+        _gpu_seen = True
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -148,6 +161,11 @@ def _arg(x, where: str, name: str, dtypes, numel: int, optional: bool = False) -
     `dtypes`, `numel` elements.  A size mismatch is SQ_ERR_INVALID (as the
     library reports for sizes it can check), a wrong dtype a TypeError.  Raw
     integer pointers are passed through unchecked."""
+    # the usual argument, in few steps (a call on small tensors takes as long
+    # as its checks)
+    if (type(x) is torch.Tensor and x.is_cuda and x.dtype in dtypes and x.numel() == numel
+            and x.is_contiguous()):
+        return
     if x is None:
         if optional:
             return
@@ -343,6 +361,8 @@ def sq_decode_step_linear(pool: SqPool, slot_ids, q, k, v, alpha, beta, o=None, 
 def _rows(x, where: str, name: str, dtype, shape) -> int:
     """Check a [tokens][heads][d] tensor whose tokens may lie further apart
     than their elements (a part of a wider buffer); returns that distance."""
+    if type(x) is torch.Tensor and x.is_cuda and x.dtype is dtype and x.shape == shape and x.is_contiguous():
+        return shape[1] * shape[2]
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{where}: {name} must be a torch tensor")
     if x.dtype != dtype:
@@ -393,8 +413,8 @@ def sq_prefill(q, k, v, alpha, beta, cu_seqlens, o, S=None, S0=None, rule: int =
     _arg(S0, w, "S0", (torch.float32,), n_seq * H * dk * dv, optional=True)
     ws, nb = _workspace(workspace, w)
     d = SqPrefillDesc(n_seq, N, H, Hk, dk, dv, code, int(rule), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                      qs, ks, vs, _ptr(alpha), _ptr(beta), _ptr(cu_seqlens), _ptr(S0), _ptr(o), _ptr(S),
-                      ws, nb)
+                      qs, ks, vs, _ptr(alpha), _ptr(beta), _ptr(cu_seqlens),
+                      None if S0 is None else _ptr(S0), _ptr(o), None if S is None else _ptr(S), ws, nb)
     _check(_lib.sq_prefill(ctypes.byref(d), _stream(stream)), w)
 
 
