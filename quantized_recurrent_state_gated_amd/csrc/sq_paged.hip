@@ -233,7 +233,9 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a)
     constexpr int TV = 16 / (int)sizeof(T);  // elements of 16 bytes
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int64_t slot[TT];
-    __shared__ uint8_t kind[TT];  // 0 skip or covered, 1 single, 2 first of a whole piece
+    __shared__ uint8_t single_at[TT], whole_at[TT];
+    __shared__ int n_single, n_whole;
+    static_assert(TT <= 64, "one wave sorts the tokens");
     const int d = a.c.d, heads = a.c.heads, P = 1 << a.c.page_shift;
     const int pitch = d + TV;     // rows stay 16-byte aligned
     T *vt = reinterpret_cast<T *>(smem);
@@ -248,16 +250,23 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a)
         slot[t] = s;
     }
     __syncthreads();
-    for (int t = threadIdx.x; t < TT; t += 256) {
-        const int64_t s = slot[t];
-        int c = 0;
+    if (threadIdx.x < 64) {
+        const int t = threadIdx.x;
+        const int64_t s = t < TT ? slot[t] : -1;
+        int c = 0;  // 1: written by itself, 2: first token of a whole piece, 0: skipped, or in such a piece
         if (s >= 0) {
             const int e = (int)(s & (TV - 1));  // place in its piece, whose first token is t - e
             bool whole = t >= e && t - e + TV <= TT;
             for (int i = 0; i < TV && whole; i++) whole = slot[t - e + i] == s - e + i;
             c = !whole ? 1 : e == 0 ? 2 : 0;
         }
-        kind[t] = (uint8_t)c;
+        const uint64_t m1 = __ballot(c == 1), m2 = __ballot(c == 2), below = (1ull << t) - 1;
+        if (c == 1) single_at[__popcll(m1 & below)] = (uint8_t)t;
+        if (c == 2) whole_at[__popcll(m2 & below)] = (uint8_t)t;
+        if (t == 0) {
+            n_single = __popcll(m1);
+            n_whole = __popcll(m2);
+        }
     }
     const int per = d / TV;  // 16-byte pieces of a row
     const T *ksrc = reinterpret_cast<const T *>(a.k), *vsrc = reinterpret_cast<const T *>(a.v);
@@ -273,23 +282,23 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a)
         *reinterpret_cast<uint4 *>(kc + row * d + x) = kk;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < nt * d; i += 256) {
-        const int t = i / d, x = i - t * d;
-        const int c = kind[t];
-        if (c == 0) continue;
+    // whole pieces: neighbouring lanes take neighbouring pieces of one column, so
+    // that a tile's tokens leave as whole lines of the page
+    for (int i = threadIdx.x; i < n_whole * d; i += 256) {
+        const int x = i / n_whole, t = whole_at[i - x * n_whole];
         const int64_t s = slot[t];
-        T *dst = vc + (((s >> a.c.page_shift) * heads + h) * d + x) * P + (s & (P - 1));
-        if (c == 1) {
-            *dst = vt[t * pitch + x];
-        } else {
-            union {
-                T e[TV];
-                uint4 w;
-            } u;
+        union {
+            T e[TV];
+            uint4 w;
+        } u;
 #pragma unroll
-            for (int j = 0; j < TV; j++) u.e[j] = vt[(t + j) * pitch + x];
-            *reinterpret_cast<uint4 *>(dst) = u.w;
-        }
+        for (int j = 0; j < TV; j++) u.e[j] = vt[(t + j) * pitch + x];
+        *reinterpret_cast<uint4 *>(vc + (((s >> a.c.page_shift) * heads + h) * d + x) * P + (s & (P - 1))) = u.w;
+    }
+    for (int i = threadIdx.x; i < n_single * d; i += 256) {
+        const int k = i / d, x = i - k * d, t = single_at[k];
+        const int64_t s = slot[t];
+        vc[(((s >> a.c.page_shift) * heads + h) * d + x) * P + (s & (P - 1))] = vt[t * pitch + x];
     }
 }
 
@@ -304,8 +313,9 @@ void append_t(const AppendArgs &a, hipStream_t st)
 template <typename T>
 void append_any(const AppendArgs &a, hipStream_t st)
 {
-    // few tokens: one piece's worth per workgroup, for more workgroups
-    if ((int64_t)a.n * a.c.heads >= 16384) append_t<T, 32>(a, st);
+    // 64 tokens of bfloat16 fill the lines of a page's columns; few tokens: one
+    // piece's worth per workgroup, for more workgroups
+    if ((int64_t)a.n * a.c.heads >= 16384) append_t<T, sizeof(T) == 2 ? 64 : 32>(a, st);
     else append_t<T, 8>(a, st);
 }
 
@@ -425,12 +435,14 @@ __global__ __launch_bounds__(256) void k_attend(AttendArgs a)
     __shared__ f32x4 sm_o[3][ND][64];
 
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-    const unsigned per_r = (unsigned)(a.splits * a.q_tiles * a.c.heads);
-    const int r = (int)(blockIdx.x / per_r);
-    unsigned rest = blockIdx.x - (unsigned)r * per_r;
-    const int sp = (int)(rest % (unsigned)a.splits);
-    rest /= (unsigned)a.splits;
-    const int qt = (int)(rest % (unsigned)a.q_tiles), h = (int)(rest / (unsigned)a.q_tiles);
+    // Workgroups go to the eight XCDs in turn.  Splits are the slowest index: later
+    // splits, which only long requests have, spread over all of them (as the
+    // fastest of eight, each XCD had one split of every request, and the last ones
+    // stood idle: 589 us against 431 at 70 requests x 8 heads up to 16 Ki tokens).
+    const unsigned units = (unsigned)(a.n * a.c.heads);
+    const unsigned unit = blockIdx.x % units, rest = blockIdx.x / units;
+    const int r = (int)(unit / (unsigned)a.c.heads), h = (int)(unit % (unsigned)a.c.heads);
+    const int qt = (int)(rest % (unsigned)a.q_tiles), sp = (int)(rest / (unsigned)a.q_tiles);
 
     const Span s = span_of(a, r);
     const int32_t begin = s.from + sp * a.chunk;
@@ -636,45 +648,64 @@ __global__ __launch_bounds__(256) void k_attend(AttendArgs a)
     }
 }
 
-// Join of the splits: one wave per (request, query head).
+// Join of the splits, a workgroup per (request, query head): the four waves take
+// every fourth split, four of them in flight.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a)
 {
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= (int64_t)a.n * a.q_heads) return;
-    const int lane = threadIdx.x & 63;
+    constexpr int PER = (D + 63) / 64, IN = 4;
+    __shared__ float sm_o[4][PER * 64], sm_l[4], sm_m[4];
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const Span s = span_of(a, (int)(row / a.q_heads));
     if (s.splits <= 1) return;  // written already
     const float *ml = a.part + (int64_t)a.n * a.q_heads * a.splits * D + row * a.splits * 2;
     float M = -__builtin_inff();
-    for (int i = lane; i < s.splits; i += 64) M = fmaxf(M, ml[2 * i]);
+    for (int i = threadIdx.x; i < s.splits; i += 256) M = fmaxf(M, ml[2 * i]);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) M = fmaxf(M, __shfl_xor(M, d));
-    constexpr int PER = (D + 63) / 64;
+    if (lane == 0) sm_m[wv] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
     float o[PER], L = 0.0f;
 #pragma unroll
     for (int j = 0; j < PER; j++) o[j] = 0.0f;
     const float *src = a.part + row * a.splits * D;
-    for (int i = 0; i < s.splits; i++) {
-        const float mi = ml[2 * i];
-        const float f = mi == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mi - M);
-        L = fmaf(ml[2 * i + 1], f, L);
+    for (int i0 = wv; i0 < s.splits; i0 += 4 * IN) {
+        float m[IN], l[IN], x[IN][PER];
 #pragma unroll
-        for (int j = 0; j < PER; j++) {
-            const int d = j * 64 + lane;
-            if (d < D) o[j] = fmaf(src[(int64_t)i * D + d], f, o[j]);
+        for (int u = 0; u < IN; u++) {
+            const int i = i0 + 4 * u;
+            const bool in = i < s.splits;
+            m[u] = in ? ml[2 * i] : -__builtin_inff();
+            l[u] = in ? ml[2 * i + 1] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < PER; j++) {
+                const int d = j * 64 + lane;
+                x[u][j] = in && d < D ? src[(int64_t)i * D + d] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < IN; u++) {
+            const float f = m[u] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[u] - M);
+            L = fmaf(l[u], f, L);
+#pragma unroll
+            for (int j = 0; j < PER; j++) o[j] = fmaf(x[u][j], f, o[j]);
         }
     }
+#pragma unroll
+    for (int j = 0; j < PER; j++) sm_o[wv][j * 64 + lane] = o[j];
+    if (lane == 0) sm_l[wv] = L;
+    __syncthreads();
+    L = sm_l[0] + sm_l[1] + sm_l[2] + sm_l[3];
     const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
     T *dst = reinterpret_cast<T *>(a.o) + row * D;
-#pragma unroll
-    for (int j = 0; j < PER; j++) {
-        const int d = j * 64 + lane;
-        if (d >= D) continue;
-        if constexpr (sizeof(T) == 4) dst[d] = o[j] * inv;
-        else dst[d] = __builtin_bit_cast(uint16_t, (__bf16)(o[j] * inv));
+    for (int d = threadIdx.x; d < D; d += 256) {
+        const float y = (sm_o[0][d] + sm_o[1][d] + sm_o[2][d] + sm_o[3][d]) * inv;
+        if constexpr (sizeof(T) == 4) dst[d] = y;
+        else dst[d] = __builtin_bit_cast(uint16_t, (__bf16)y);
     }
-    if (a.lse && lane == 0)
+    if (a.lse && threadIdx.x == 0)
         a.lse[row] = L == 0.0f ? -__builtin_inff() : (M + __builtin_log2f(L)) * 0.69314718055994531f;
 }
 
@@ -685,7 +716,7 @@ hipError_t attend_td(const AttendArgs &a, hipStream_t st)
     hipLaunchKernelGGL((k_attend<T, D>), dim3((unsigned)grid), dim3(256), 0, st, a);
     if (hipError_t e = hipGetLastError()) return e;
     if (a.splits > 1) {
-        const int64_t rows = ((int64_t)a.n * a.q_heads + 3) / 4;
+        const int64_t rows = (int64_t)a.n * a.q_heads;
         hipLaunchKernelGGL((k_attend_join<T, D>), dim3((unsigned)rows), dim3(256), 0, st, a);
     }
     return hipGetLastError();
@@ -712,18 +743,24 @@ bool attend_head_dim(int32_t d)
     return d == 32 || d == 64 || d == 96 || d == 128 || d == 192 || d == 256;
 }
 
-// Workgroups wanted of a launch, and the smallest split.
-constexpr int64_t kTarget = 2048, kMinChunk = 128;
+// Tokens per split.  Contexts of uneven length want many small workgroups to
+// fill in behind each other (70 requests x 8 heads up to 16 Ki tokens: 430 us with
+// 4096 workgroups, 445 with 1536, 478 with 1024), but every split pays for its
+// start and its join: up to 2048 tokens a split, 512 workgroups do (one request,
+// 8 heads x 100,000 tokens: 79 us with 512 workgroups, 84 with 1024, 103 with 4096; 128
+// requests x 8 heads up to 1000 tokens: 59, 62, 69).  Below 256 tokens a split's
+// start outweighs its work.
+constexpr int64_t kMost = 4096, kFew = 512, kLongSplit = 2048, kMinChunk = 256;
 
 uint64_t attend_rows_bound(int32_t n, int32_t kv_heads, int32_t q_heads, int32_t max_len)
 {
-    // splits <= (max_len + 31) / chunk + 1 with chunk >= max_len units / kTarget,
+    // splits <= (max_len + 31) / chunk + 1 with chunk >= max_len units / kMost,
     // kMinChunk <= chunk <= kMaxChunk; q_heads <= 16 x query tiles x kv_heads
     const uint64_t rows = (uint64_t)n * (uint64_t)q_heads;
     const uint64_t fine = ((uint64_t)max_len + 31 + kMinChunk - 1) / kMinChunk;
     const uint64_t coarse = ((uint64_t)max_len + 31 + kMaxChunk - 1) / kMaxChunk;
     const uint64_t group = (uint64_t)(q_heads / kv_heads), tile = group < 16 ? group : 16;
-    const uint64_t a = rows * fine, b = kTarget * tile + 2 * rows, c = rows * coarse;
+    const uint64_t a = rows * fine, b = kMost * tile + 2 * rows, c = rows * coarse;
     return a < (b > c ? b : c) ? a : (b > c ? b : c);
 }
 
@@ -731,9 +768,12 @@ void attend_split(int32_t n, int32_t heads, int32_t q_tiles, int32_t max_len, in
                   int32_t *splits)
 {
     const int64_t units = (int64_t)n * heads * q_tiles;
-    int64_t c = ((int64_t)max_len * units + kTarget - 1) / kTarget;
-    c = (c + kMinChunk - 1) / kMinChunk * kMinChunk;  // whole rounds of four waves' tiles
+    const int64_t all = (int64_t)max_len * units;
+    int64_t c = (all + kFew - 1) / kFew;
+    if (c > kLongSplit) c = kLongSplit;
+    if (c < (all + kMost - 1) / kMost) c = (all + kMost - 1) / kMost;
     if (c < kMinChunk) c = kMinChunk;
+    c = (c + 127) / 128 * 128;  // whole rounds of four waves' tiles
     if (c > kMaxChunk) c = kMaxChunk;
     *chunk = (int32_t)c;
     // a window's first tile may start up to 31 tokens before it
