@@ -46,35 +46,58 @@ __device__ __forceinline__ Seq seq_of(const PrefillArgs &a, int s)
     return r;
 }
 
+// the shared-memory barrier alone: loads and stores in flight to global memory
+// (the next chunk's inputs, this chunk's outputs) are not waited for
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // ---------------------------------------------------------------- token by token
 //
-// Any d_k, d_v (multiples of 4, at most 256) and both element types: one
-// workgroup per (sequence, head, 64 columns), four lanes per column, each
-// holding RPL rows of it in registers.  The columns of S are independent of
-// each other; per token a lane does three fused multiply-adds a row for
+// Any d_k, d_v (multiples of 4, at most 256) and both element types.  The
+// columns of S are independent of each other: LPC lanes hold a column, RPL rows
+// each, in registers.  Per token a lane does three fused multiply-adds a row for
 //     u = k^T S, y = q^T S, and the update S = alpha S + k w,
 //     w = beta (v - alpha u), o = alpha y + (q.k) w,
-// and the four lanes join their sums with two exchanges.  Tokens are staged
-// through shared memory TB at a time.
+// and the column's lanes join their sums by DPP exchanges.  Tokens, with their
+// q.k, are staged through shared memory TB at a time.  A token takes as long as
+// its chain of instructions: 16 lanes a column where workgroups are few
+// (36 heads x 77 tokens of fp32, d = 128: 30 us against 46 with 4; 48 heads x 400
+// tokens 127 against 214), 4 where there are enough of them and the exchanges only
+// cost (384 heads x 200 tokens 176 us against 250).
 
 constexpr int kTB = 16;  // tokens staged at a time
 
-__device__ __forceinline__ float quad_sum(float x)
+template <int CTRL>
+__device__ __forceinline__ float dpp_sum(float x)
 {
-    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0xb1, 0xf, 0xf, false));
-    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x4e, 0xf, 0xf, false));
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, false));
+}
+
+// sum over LPC neighbouring lanes, in all of them
+template <int LPC>
+__device__ __forceinline__ float lanes_sum(float x)
+{
+    x = dpp_sum<0xb1>(x);                        // quad_perm [1,0,3,2]
+    x = dpp_sum<0x4e>(x);                        // quad_perm [2,3,0,1]
+    if constexpr (LPC >= 8) x = dpp_sum<0x141>(x);   // row_half_mirror: sums of 8
+    if constexpr (LPC >= 16) x = dpp_sum<0x140>(x);  // row_mirror: sums of 16
     return x;
 }
 
-template <typename T, bool DELTA, int RPL>
+template <typename T, bool DELTA, int LPC, int RPL>
 __global__ __launch_bounds__(256) void k_prefill_tokens(PrefillArgs a)
 {
-    constexpr int ROWS = 4 * RPL;
+    constexpr int ROWS = LPC * RPL, COLS = 256 / LPC;
     __shared__ __align__(16) float sq[kTB][ROWS], sk[kTB][ROWS];
-    __shared__ float sv[kTB][64], sg[kTB][2];
-    const int t = threadIdx.x, part = t & 3, col = t >> 2;
-    const int tiles = (a.dv + 63) / 64;
-    const int j0 = (int)(blockIdx.x % (unsigned)tiles) * 64;
+    __shared__ float sv[kTB][COLS];
+    __shared__ float4 sg[kTB];  // alpha, beta, q.k
+    const int t = threadIdx.x, part = t % LPC, col = t / LPC;
+    const int tiles = (a.dv + COLS - 1) / COLS;
+    const int j0 = (int)(blockIdx.x % (unsigned)tiles) * COLS;
     const int sh = (int)(blockIdx.x / (unsigned)tiles);
     const int h = sh % a.heads, s = sh / a.heads;
     const Seq sr = seq_of(a, s);
@@ -82,11 +105,11 @@ __global__ __launch_bounds__(256) void k_prefill_tokens(PrefillArgs a)
     const bool in = j < a.dv;
     const int64_t tile = (int64_t)sh * a.dk * a.dv;
 
-    // row 16 i + 4 part + e
+    // row 4 (LPC i + part) + e
     float S[RPL];
 #pragma unroll
     for (int i = 0; i < RPL; i++) {
-        const int row = 16 * (i >> 2) + 4 * part + (i & 3);
+        const int row = 4 * (LPC * (i >> 2) + part) + (i & 3);
         S[i] = a.S0 && in && row < a.dk ? a.S0[tile + (int64_t)row * a.dv + j] : 0.0f;
     }
     const T *q = reinterpret_cast<const T *>(a.q) + (int64_t)(h / a.per_k) * a.dk;
@@ -94,69 +117,103 @@ __global__ __launch_bounds__(256) void k_prefill_tokens(PrefillArgs a)
     const T *v = reinterpret_cast<const T *>(a.v) + (int64_t)h * a.dv;
     T *o = reinterpret_cast<T *>(a.o) + (int64_t)h * a.dv;
 
+    // 16 lanes a token bring it, 16 tokens at once, a block ahead of its use
+    constexpr int NQ = ROWS / 16, NV = COLS / 16;
+    const int bx = t >> 4, bl = t & 15;
+    float nq[NQ], nk[NQ], nv[NV], na = 0.0f, nb = 0.0f;
+    auto bring = [&](int32_t t0) {
+        const int64_t tok = t0 + bx;
+        if (tok >= sr.last) return;
+#pragma unroll
+        for (int i = 0; i < NQ; i++) {
+            const int d = 16 * i + bl;
+            nq[i] = d < a.dk ? up<T>(q[tok * a.q_stride + d]) : 0.0f;
+            nk[i] = d < a.dk ? up<T>(k[tok * a.k_stride + d]) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int d = 16 * i + bl;
+            nv[i] = j0 + d < a.dv ? up<T>(v[tok * a.v_stride + j0 + d]) : 0.0f;
+        }
+        if (bl == 0) {
+            na = a.alpha[tok * a.heads + h];
+            nb = a.beta[tok * a.heads + h];
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NQ; i++) nq[i] = nk[i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; i++) nv[i] = 0.0f;
+    bring(sr.first);
     for (int32_t t0 = sr.first; t0 < sr.last; t0 += kTB) {
         const int nt = sr.last - t0 < kTB ? sr.last - t0 : kTB;
-        __syncthreads();
-        for (int i = t; i < nt * ROWS; i += 256) {
-            const int x = i / ROWS, d = i % ROWS;
-            const int64_t tok = t0 + x;
-            sq[x][d] = d < a.dk ? up<T>(q[tok * a.q_stride + d]) : 0.0f;
-            sk[x][d] = d < a.dk ? up<T>(k[tok * a.k_stride + d]) : 0.0f;
+        {
+            float dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NQ; i++) {
+                sq[bx][16 * i + bl] = nq[i];
+                sk[bx][16 * i + bl] = nk[i];
+                dot = fmaf(nq[i], nk[i], dot);
+            }
+#pragma unroll
+            for (int i = 0; i < NV; i++) sv[bx][16 * i + bl] = nv[i];
+            dot = lanes_sum<16>(dot);
+            if (bl == 0) sg[bx] = make_float4(na, nb, dot, 0.0f);
         }
-        for (int i = t; i < nt * 64; i += 256) {
-            const int x = i >> 6, d = i & 63;
-            sv[x][d] = j0 + d < a.dv ? up<T>(v[(int64_t)(t0 + x) * a.v_stride + j0 + d]) : 0.0f;
-        }
-        if (t < nt) {
-            sg[t][0] = a.alpha[(int64_t)(t0 + t) * a.heads + h];
-            sg[t][1] = a.beta[(int64_t)(t0 + t) * a.heads + h];
-        }
-        __syncthreads();
+        if (t0 + kTB < sr.last) bring(t0 + kTB);
+        lds_barrier();
         for (int x = 0; x < nt; x++) {
-            float u = 0.0f, y = 0.0f, qk = 0.0f, kr[RPL];
+            float u = 0.0f, y = 0.0f, kr[RPL];
 #pragma unroll
             for (int i = 0; i < RPL; i += 4) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(&sk[x][4 * i + 4 * part]);
-                const float4 q4 = *reinterpret_cast<const float4 *>(&sq[x][4 * i + 4 * part]);
+                const float4 k4 = *reinterpret_cast<const float4 *>(&sk[x][LPC * i + 4 * part]);
+                const float4 q4 = *reinterpret_cast<const float4 *>(&sq[x][LPC * i + 4 * part]);
                 const float qe[4] = {q4.x, q4.y, q4.z, q4.w};
                 kr[i] = k4.x; kr[i + 1] = k4.y; kr[i + 2] = k4.z; kr[i + 3] = k4.w;
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     if (DELTA) u = fmaf(kr[i + e], S[i + e], u);
                     y = fmaf(qe[e], S[i + e], y);
-                    qk = fmaf(qe[e], kr[i + e], qk);
                 }
             }
-            if (DELTA) u = quad_sum(u);
-            y = quad_sum(y);
-            qk = quad_sum(qk);
-            const float al = sg[x][0], vj = sv[x][col];
-            const float w = sg[x][1] * (DELTA ? vj - al * u : vj);
+            if (DELTA) u = lanes_sum<LPC>(u);
+            y = lanes_sum<LPC>(y);
+            const float4 gt = sg[x];
+            const float vj = sv[x][col];
+            const float w = gt.y * (DELTA ? vj - gt.x * u : vj);
 #pragma unroll
-            for (int i = 0; i < RPL; i++) S[i] = fmaf(al, S[i], kr[i] * w);
-            if (part == 0 && in)
-                o[(int64_t)(t0 + x) * a.heads * a.dv + j] = down<T>(fmaf(al, y, qk * w));
+            for (int i = 0; i < RPL; i++) S[i] = fmaf(gt.x, S[i], kr[i] * w);
+            if (part == 0 && in) o[(int64_t)(t0 + x) * a.heads * a.dv + j] = down<T>(fmaf(gt.x, y, gt.z * w));
         }
+        lds_barrier();
     }
     if (!a.S || !in) return;
 #pragma unroll
     for (int i = 0; i < RPL; i++) {
-        const int row = 16 * (i >> 2) + 4 * part + (i & 3);
+        const int row = 4 * (LPC * (i >> 2) + part) + (i & 3);
         if (row < a.dk) a.S[tile + (int64_t)row * a.dv + j] = S[i];
     }
+}
+
+template <typename T, bool DELTA, int LPC>
+hipError_t tokens_l(const PrefillArgs &a, hipStream_t st)
+{
+    constexpr int COLS = 256 / LPC;
+    const unsigned grid = (unsigned)((int64_t)a.n_seq * a.heads * ((a.dv + COLS - 1) / COLS));
+    if (a.dk <= 64)
+        hipLaunchKernelGGL((k_prefill_tokens<T, DELTA, LPC, 64 / LPC>), dim3(grid), dim3(256), 0, st, a);
+    else if (a.dk <= 128)
+        hipLaunchKernelGGL((k_prefill_tokens<T, DELTA, LPC, 128 / LPC>), dim3(grid), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_prefill_tokens<T, DELTA, LPC, 256 / LPC>), dim3(grid), dim3(256), 0, st, a);
+    return hipGetLastError();
 }
 
 template <typename T, bool DELTA>
 hipError_t tokens_t(const PrefillArgs &a, hipStream_t st)
 {
-    const unsigned grid = (unsigned)((int64_t)a.n_seq * a.heads * ((a.dv + 63) / 64));
-    if (a.dk <= 64)
-        hipLaunchKernelGGL((k_prefill_tokens<T, DELTA, 16>), dim3(grid), dim3(256), 0, st, a);
-    else if (a.dk <= 128)
-        hipLaunchKernelGGL((k_prefill_tokens<T, DELTA, 32>), dim3(grid), dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL((k_prefill_tokens<T, DELTA, 64>), dim3(grid), dim3(256), 0, st, a);
-    return hipGetLastError();
+    if ((int64_t)a.n_seq * a.heads * a.dv <= 12288) return tokens_l<T, DELTA, 16>(a, st);
+    return tokens_l<T, DELTA, 4>(a, st);
 }
 
 // ---------------------------------------------------------------- chunked form, d = 128, bfloat16
@@ -266,15 +323,6 @@ struct SmemChunkDelta : SmemChunk {
 __device__ __forceinline__ bf16x8 lds16(const unsigned char *p)
 {
     return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(p));
-}
-
-// the shared-memory barrier alone: loads and stores in flight to global memory
-// (the next chunk's inputs, this chunk's outputs) are not waited for
-__device__ __forceinline__ void lds_barrier()
-{
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
 }
 
 // order of one wave's own shared-memory accesses across its lanes (the
@@ -543,9 +591,19 @@ __device__ __forceinline__ int nth_longest(const PrefillArgs &a, int n, int lane
 // and queries to shared memory and compute the gates, P, T and N of the chunks
 // to come.  One barrier a chunk.  Inputs are read once, and no intermediate
 // leaves the CU.
-template <bool DELTA, int NW>
+//
+// STEP.  kWhole: a workgroup takes a whole sequence.  With a plain decay the
+// state after a segment is a sum, decay x (state before) + (what the segment
+// writes), so long sequences of few heads are cut into segments of a.seg chunks:
+// kWrites leaves what each segment writes from zero, and its decay, in the
+// workspace, and kSegment then starts each segment from the sum of those before
+// it.  The first pass needs neither queries nor outputs: two fifths of the work.
+enum Step { kWhole, kWrites, kSegment };
+
+template <bool DELTA, int NW, int STEP>
 __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
 {
+    static_assert(STEP == kWhole || !DELTA, "the delta rule's segments do not add up");
     using SM = typename std::conditional<DELTA, SmemChunkDelta, SmemChunk>::type;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     SM &sm = *reinterpret_cast<SM *>(smem_raw);
@@ -556,9 +614,28 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
     // column splits of a head next to each other
     const int split = (int)(blockIdx.x % (unsigned)(8 / NW));
     const unsigned rest = blockIdx.x / (unsigned)(8 / NW);
-    const int h = (int)(rest % (unsigned)a.heads), s = nth_longest(a, (int)(rest / (unsigned)a.heads), lane);
+    const int h = (int)(rest % (unsigned)a.heads);
+    int s, segment = 0, more = 0;  // the segment's number, and how many follow it
+    Seq sr;
+    if constexpr (STEP == kWhole) {
+        s = nth_longest(a, (int)(rest / (unsigned)a.heads), lane);
+        sr = seq_of(a, s);
+    } else {
+        // segment i of sequence s is record first / length + s + i: records of
+        // different sequences are disjoint
+        const int rec = (int)(rest / (unsigned)a.heads), length = a.seg * kC;
+        for (s = 0; s + 1 < a.n_seq && seq_of(a, s + 1).first / length + s + 1 <= rec;) s++;
+        sr = seq_of(a, s);
+        segment = rec - (sr.first / length + s);
+        const int64_t from = sr.first + (int64_t)segment * length;
+        if (segment < 0 || (from >= sr.last && segment > 0)) return;
+        // the last segment's writes are not asked for
+        if (STEP == kWrites && from + length >= sr.last) return;
+        sr.first = (int32_t)from;
+        more = (sr.last - sr.first - 1) / length;
+    }
+    if (more > 0) sr.last = sr.first + a.seg * kC;
     const int64_t sh = (int64_t)s * a.heads + h;
-    const Seq sr = seq_of(a, s);
     const int chunks = (sr.last - sr.first + kC - 1) / kC;
     // row strides in bytes (the host has checked that 64 rows are below 2^31)
     const int32_t ks2 = (int32_t)a.k_stride * 2, qs2 = (int32_t)a.q_stride * 2, vs2 = (int32_t)a.v_stride * 2;
@@ -578,6 +655,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
     if (wv >= NW) {
         if (chunks == 0) return;
         const int role = wv - NW;
+        if (STEP == kWrites && role >= 2) return;
         // an operand's pieces straight from global memory: rows perm(m, c)
         auto rows = [&](__amdgpu_buffer_rsrc_t w, int32_t st, int m, bf16x8 (&f)[4]) {
             const int32_t b = here(rho * st + 16 * g) + perm(m, 0) * st;
@@ -591,7 +669,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
             // 0: keys, and N (plain decay: half of P); 1: queries, gates and (delta) half of P.
             // The wave reads back, as operands, rows that it has written itself.
             float al = 1.0f, bt = 0.0f;
-            constexpr int PROLE = DELTA ? 1 : 0;
+            constexpr int PROLE = STEP == kWrites ? -1 : DELTA ? 1 : 0;
             auto gates = [&](int n) {
                 const bool in = lane < tokens_of(n);
                 const int64_t i = (first_of(n) + lane) * a.heads + h;
@@ -609,10 +687,11 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
 #pragma unroll
                 for (int u = 0; u < 16; u++) x[u] = __builtin_amdgcn_raw_buffer_load_b128(w, b + 4 * u * st, 0, 0);
             };
-            load_rows(0);
+            const bool brings = STEP != kWrites || role == 0;
+            if (brings) load_rows(0);
             for (int n = -2; n < chunks; n++) {
                 lds_barrier();
-                if (n + 1 >= 0 && n + 1 < chunks) {
+                if (brings && n + 1 >= 0 && n + 1 < chunks) {
                     const auto kw = key_window(n + 1), qw = query_window(n + 1);
                     bf16x8 f[2][4];
                     if (role == PROLE) {
@@ -718,7 +797,39 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
 #pragma unroll
     for (int m = 0; m < 8; m++)
 #pragma unroll
-        for (int r = 0; r < 4; r++) S[m][r] = a.S0 ? a.S0[tile + (int64_t)perm(m, 4 * g + r) * kD] : 0.0f;
+        for (int r = 0; r < 4; r++)
+            S[m][r] = a.S0 && (STEP == kWhole || segment == 0) ? a.S0[tile + (int64_t)perm(m, 4 * g + r) * kD] : 0.0f;
+    float decay = 1.0f;  // of the whole segment
+    float *ws_decay = reinterpret_cast<float *>(a.ws);
+    float *ws_state = ws_decay + a.seg_pad;
+    const int64_t rec = (int64_t)(rest / (unsigned)a.heads) * a.heads + h;
+    auto slot = [&](int64_t record) { return ws_state + record * kD * kD + col0 + c; };
+    if constexpr (STEP != kWhole) {
+        // S may be S0, and the last segment may end before the first begins: the
+        // first pass keeps S0 in the last segment's record, which it leaves unused
+        if (segment == 0 && more > 0 && a.S0 && a.S) {
+            float *kept = slot(rec + (int64_t)more * a.heads);
+#pragma unroll
+            for (int m = 0; m < 8; m++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    float *p = kept + (int64_t)perm(m, 4 * g + r) * kD;
+                    if (STEP == kWrites) *p = S[m][r];
+                    else S[m][r] = *p;
+                }
+        }
+    }
+    if constexpr (STEP == kSegment) {
+        // (segment 0 started from S0, so its writes hold the state itself)
+        for (int i = segment; i > 0; i--) {
+            const float *src = slot(rec - (int64_t)i * a.heads);
+            const float f = ws_decay[rec - (int64_t)i * a.heads];
+#pragma unroll
+            for (int m = 0; m < 8; m++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) S[m][r] = fmaf(f, S[m][r], src[(int64_t)perm(m, 4 * g + r) * kD]);
+        }
+    }
 
     const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v) + (int64_t)h * kD + col0;
     uint16_t *o = reinterpret_cast<uint16_t *>(a.o) + (int64_t)h * kD + col0;
@@ -762,7 +873,10 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
 
         // K S, and S^T Q^T
         f32x4 O[4];
-        {
+        if constexpr (STEP == kWrites) {
+#pragma unroll
+            for (int m = 0; m < 4; m++) W[m] *= *reinterpret_cast<const f32x4 *>(&sd.be[perm(m, 4 * g)]);
+        } else {
             f32x4 KS[4];
 #pragma unroll
             for (int m = 0; m < 4; m++) O[m] = KS[m] = f32x4{0, 0, 0, 0};
@@ -795,6 +909,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
             }
         }
         const float gC = sd.gam[kC - 1];
+        if constexpr (STEP == kWrites) decay *= gC;
 #pragma unroll
         for (int m = 0; m < 8; m++) S[m] *= gC;
 #pragma unroll
@@ -831,9 +946,10 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
                         }
                     }
                 }
-            } else {
+            } else if constexpr (STEP != kWrites) {
                 planes<3>(W[m0], W[m0 + 1], wp);
             }
+            if constexpr (STEP != kWrites) {
             // O^T = 2^G (S^T Q^T) + W^T P^T
             bf16x8 p0[4], p1[4];
 #pragma unroll
@@ -847,6 +963,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
             for (int m = m0; m < 4; m++) O[m] = mma(wp[1], p0[m], O[m]);
 #pragma unroll
             for (int m = m0; m < 4; m++) O[m] = mma(wp[0], p1[m], O[m]);
+            }
             // S' = 2^G_C S + K^T (2^(G_C - G) W)
             const f32x4 d0 = *reinterpret_cast<const f32x4 *>(&sd.dec[32 * ks + 8 * g]);
             const f32x4 d1 = *reinterpret_cast<const f32x4 *>(&sd.dec[32 * ks + 8 * g + 4]);
@@ -871,6 +988,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
                     for (int i = 0; i < 4; i++) S[mh + i] = mma(kt[i], wp[p], S[mh + i]);
             }
         }
+        if constexpr (STEP != kWrites) {
         // a lane's four neighbouring columns of token perm(m, c)
         const auto ow = rows_of(o + first_of(n) * a.heads * kD, tokens_of(n), os2, 32);
 #pragma unroll
@@ -879,20 +997,31 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
             __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, __builtin_convertvector(O[m], bf16x4)),
                                                   ow, here(at_o) + perm(m, 0) * os2, 0, 0);
         }
+        }
     }
-    if (!a.S) return;
+    if constexpr (STEP == kWrites) {
+        float *dst = slot(rec);
+#pragma unroll
+        for (int m = 0; m < 8; m++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) dst[(int64_t)perm(m, 4 * g + r) * kD] = S[m][r];
+        // (every wave writes the same decay)
+        if (lane == 0) ws_decay[rec] = decay;
+        return;
+    }
+    if (!a.S || more > 0) return;
 #pragma unroll
     for (int m = 0; m < 8; m++)
 #pragma unroll
         for (int r = 0; r < 4; r++) a.S[tile + (int64_t)perm(m, 4 * g + r) * kD] = S[m][r];
 }
 
-template <bool DELTA, int NW>
-hipError_t chunks_t(const PrefillArgs &a, hipStream_t st)
+template <bool DELTA, int NW, int STEP>
+hipError_t chunks_t(const PrefillArgs &a, int64_t units, hipStream_t st)
 {
-    const unsigned grid = (unsigned)((int64_t)a.n_seq * a.heads * (8 / NW));
+    const unsigned grid = (unsigned)(units * a.heads * (8 / NW));
     const size_t lds = DELTA ? sizeof(SmemChunkDelta) : sizeof(SmemChunk);
-    auto kern = k_prefill_chunks<DELTA, NW>;
+    auto kern = k_prefill_chunks<DELTA, NW, STEP>;
     if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
         return e;
@@ -900,15 +1029,49 @@ hipError_t chunks_t(const PrefillArgs &a, hipStream_t st)
     return hipGetLastError();
 }
 
+// How a plain decay's sequences are cut: chunks per segment (0: not), and the
+// number of segment records.  Worth it while the heads of all sequences leave
+// CUs idle and there is something to cut (48 heads x 16 Ki tokens 330 us against
+// 700 uncut); the segments then fill the 256 CUs once.
+struct Cut {
+    int32_t seg;
+    int64_t records;
+};
+constexpr int32_t kCutHeads = 64, kSegMin = 16;
+
+Cut cut_of(int32_t n_seq, int32_t n_tokens, int32_t heads)
+{
+    const int64_t sh = (int64_t)n_seq * heads, chunks = ((int64_t)n_tokens + kC - 1) / kC;
+    if (sh > kCutHeads || chunks < 2 * kSegMin) return Cut{0, 0};
+    int64_t seg = (chunks * heads + 255 - sh) / (256 - sh);
+    if (seg < kSegMin) seg = kSegMin;
+    return Cut{(int32_t)seg, (int64_t)n_tokens / (seg * kC) + n_seq + 1};
+}
+
+// decays, padded to whole lines, then states
+int64_t cut_pad(int64_t rows) { return (rows + 63) / 64 * 64; }
+uint64_t cut_bytes(int64_t rows) { return 4 * ((uint64_t)cut_pad(rows) + (uint64_t)rows * kD * kD); }
+
 template <bool DELTA>
 hipError_t chunked(const PrefillArgs &a, hipStream_t st)
 {
+    if constexpr (!DELTA) {
+        const Cut cut = cut_of(a.n_seq, a.n_tokens, a.heads);
+        if (cut.seg > 0) {
+            PrefillArgs b = a;
+            b.seg = cut.seg;
+            b.seg_pad = cut_pad(cut.records * a.heads);
+            if (hipError_t e = chunks_t<false, 8, kWrites>(b, cut.records, st)) return e;
+            return chunks_t<false, 8, kSegment>(b, cut.records, st);
+        }
+    }
     // One workgroup fits a CU.  While the halves of all heads fit the 256 CUs
     // together, two workgroups a head are faster (a step of fewer columns: delta,
     // 96 heads x 4,096 tokens 310 us against 421, 48 heads 290 against 374; quarters
     // 578 and 298); above that, whole heads, whose common work is done once
     // (144 heads 431 us against 599, 192 heads 453 against 609).
-    return (int64_t)a.n_seq * a.heads <= 128 ? chunks_t<DELTA, 4>(a, st) : chunks_t<DELTA, 8>(a, st);
+    return (int64_t)a.n_seq * a.heads <= 128 ? chunks_t<DELTA, 4, kWhole>(a, a.n_seq, st)
+                                             : chunks_t<DELTA, 8, kWhole>(a, a.n_seq, st);
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
@@ -924,16 +1087,37 @@ bool chunk_aligned(const PrefillArgs &a)
            a.v_stride <= kMost && (int64_t)a.heads * kD <= kMost;
 }
 
+bool takes_chunks(const PrefillArgs &a, bool bf16)
+{
+    // A few tokens a sequence go faster one by one than as a padded chunk (768 heads,
+    // 8 tokens each: 35 us against 42; 16 tokens 49 against 43).
+    const bool few = a.n_tokens <= 12 * (int64_t)a.n_seq;
+    return chunk_shape(a.dk, a.dv, bf16) && chunk_aligned(a) && !few;
+}
+
 }  // namespace
 
-uint64_t prefill_workspace(int32_t, int32_t, int32_t, int32_t, int32_t, bool, bool) { return 0; }
+uint64_t prefill_workspace(int32_t n_seq, int32_t n_tokens, int32_t heads, int32_t dk, int32_t dv, bool bf16,
+                           bool delta)
+{
+    // for every call with at most these sizes: records x heads <= min(n_tokens /
+    // (64 kSegMin) heads, 256) + n_seq heads + heads, n_seq heads <= kCutHeads
+    if (!chunk_shape(dk, dv, bf16) || delta || n_tokens < 2 * kSegMin * kC - kC + 1) return 0;
+    const int64_t by_tokens = (int64_t)n_tokens / (kSegMin * kC) * heads, sh = (int64_t)n_seq * heads;
+    return cut_bytes((by_tokens < 256 ? by_tokens : 256) + (sh < kCutHeads ? sh : kCutHeads) +
+                     (heads < kCutHeads ? heads : kCutHeads));
+}
+
+uint64_t prefill_needs(const PrefillArgs &a, bool bf16, bool delta)
+{
+    if (!takes_chunks(a, bf16) || delta) return 0;
+    const Cut cut = cut_of(a.n_seq, a.n_tokens, a.heads);
+    return cut.seg > 0 ? cut_bytes(cut.records * a.heads) : 0;
+}
 
 hipError_t launch_prefill(const PrefillArgs &a, bool bf16, bool delta, hipStream_t st)
 {
-    // A few tokens a sequence go faster one by one than as a padded chunk (768 heads,
-    // 8 tokens each: 33 us against 42; 16 tokens 49 against 43).
-    const bool few = a.n_tokens <= 12 * (int64_t)a.n_seq;
-    if (chunk_shape(a.dk, a.dv, bf16) && chunk_aligned(a) && !few) return delta ? chunked<true>(a, st) : chunked<false>(a, st);
+    if (takes_chunks(a, bf16)) return delta ? chunked<true>(a, st) : chunked<false>(a, st);
     if (bf16) return delta ? tokens_t<uint16_t, true>(a, st) : tokens_t<uint16_t, false>(a, st);
     return delta ? tokens_t<float, true>(a, st) : tokens_t<float, false>(a, st);
 }

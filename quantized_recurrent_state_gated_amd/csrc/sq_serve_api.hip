@@ -225,10 +225,6 @@ int sq_prefill(const sq_prefill_desc *desc, void *stream)
             return SQ_ERR_INVALID;
     }
     if (!aligned(d.S0, 16) || !aligned(d.S, 16)) return SQ_ERR_INVALID;
-    const uint64_t need = sqk::prefill_workspace(d.n_seq, d.n_tokens, d.n_heads, d.d_k, d.d_v,
-                                                 d.dtype == SQ_BF16, d.rule == SQ_RULE_DELTA);
-    if (need > 0 && (!d.workspace || d.workspace_bytes < need || !aligned(d.workspace, 256)))
-        return SQ_ERR_INVALID;
     if ((int64_t)d.n_seq * d.n_heads > kMaxGrid / 64 ||
         ((int64_t)d.n_tokens / 16 + d.n_seq) > kMaxGrid / d.n_heads)
         return SQ_ERR_UNSUPPORTED;
@@ -252,6 +248,9 @@ int sq_prefill(const sq_prefill_desc *desc, void *stream)
     a.o = d.o;
     a.S = d.S;
     a.ws = static_cast<uint8_t *>(d.workspace);
+    const uint64_t need = sqk::prefill_needs(a, d.dtype == SQ_BF16, d.rule == SQ_RULE_DELTA);
+    if (need > 0 && (!d.workspace || d.workspace_bytes < need || !aligned(d.workspace, 256)))
+        return SQ_ERR_INVALID;
     return status(sqk::launch_prefill(a, d.dtype == SQ_BF16, d.rule == SQ_RULE_DELTA,
                                       (hipStream_t)stream));
 }

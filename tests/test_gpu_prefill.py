@@ -123,6 +123,35 @@ def test_parts_of_one_wider_buffer(sq, dtype):
     check(sq, x, 0, dtype)
 
 
+@pytest.mark.parametrize("rule", [0, 1])
+def test_many_heads_and_many_sequences(sq, rule):
+    """Whole heads to a workgroup (more than 128 heads in all), more than 64
+    sequences, and a few tokens a sequence."""
+    check(sq, make(31, [66, 0, 130], 50, 25, 128, 128, "bf16"), rule, "bf16")
+    check(sq, make(33, [(i * 37) % 80 + (i == 7) * 64 for i in range(75)], 2, 2, 128, 128, "bf16"), rule, "bf16")
+    check(sq, make(35, [(i * 5) % 14 for i in range(20)], 3, 1, 128, 128, "bf16"), rule, "bf16")
+
+
+@pytest.mark.parametrize("lens,H", [([5000], 1), ([2100, 1024, 0, 1, 3333], 2), ([1, 1984, 64], 3), ([4097], 48)])
+def test_long_plain_decay(sq, lens, H):
+    """Sequences that are cut into segments, the state out of place and in place."""
+    x = make(len(lens) + H, lens, H, H, 128, 128, "bf16")
+    x["alpha"][:, 0] = 0.9999  # something is left of the segments before
+    o, S = check(sq, x, 1, "bf16")
+    state = x["S0"].cuda()
+    N, n = sum(lens), len(lens)
+    po = torch.empty(N, H, 128, dtype=torch.bfloat16, device="cuda")
+    nb = sq.sq_prefill_workspace(n, N, H, 128, 128, torch.bfloat16, 1)
+    assert nb > 0
+    sq.sq_prefill(*(x[k].cuda() for k in ("q", "k", "v", "alpha", "beta")), torch.from_numpy(x["cu"]).cuda(), po,
+                  S=state, S0=state, rule=1, workspace=torch.full((nb,), 0xff, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert np.array_equal(state.cpu().numpy(), S) and np.array_equal(po.float().cpu().numpy(), o)
+    with pytest.raises(sq.SqError):
+        sq.sq_prefill(*(x[k].cuda() for k in ("q", "k", "v", "alpha", "beta")), torch.from_numpy(x["cu"]).cuda(), po,
+                      S=state, S0=state, rule=1)
+
+
 @pytest.mark.parametrize("keys", ["alike", "same"])
 def test_keys_that_lie_close(sq, keys):
     """Nearly parallel keys with full write strength: the inverse of the

@@ -95,13 +95,18 @@ def test_prefill_workspace_is_enforced_and_grows(sq):
         for rule in (0, 1):
             f = lambda *a: sq.sq_prefill_workspace(*a, 128, 128, dtype, rule)  # noqa: E731
             assert f(1, 64, 2) <= f(2, 64, 2) <= f(2, 500, 2) <= f(2, 500, 5)
-    nb = sq.sq_prefill_workspace(2, 100, 4, 128, 128, torch.bfloat16, 0)
-    d = dict(n_seq=2, n_tokens=100, n_heads=4, n_k_heads=4, d_k=128, d_v=128, dtype=1, rule=0, q=A, k=A, v=A,
+            sizes = [(1, 64, 2), (1, 1984, 2), (1, 1985, 2), (1, 5000, 2), (2, 5000, 2), (2, 5000, 40), (2, 5000, 90),
+                     (300, 5000, 90), (300, 500000, 90)]
+            for a, b in zip(sizes, sizes[1:]):
+                assert f(*a) <= f(*b)
+    # a long plain decay of few heads is cut into segments, through the workspace
+    d = dict(n_seq=1, n_tokens=5000, n_heads=4, n_k_heads=4, d_k=128, d_v=128, dtype=1, rule=1, q=A, k=A, v=A,
              q_stride=512, k_stride=512, v_stride=512, alpha=A, beta=A, cu_seqlens=A, o=A)
-    if nb:
-        for ws, size in ((None, nb), (A, nb - 1), (A + 16, nb)):
-            x = sq.SqPrefillDesc(**d, workspace=ws, workspace_bytes=size)
-            assert sq._lib.sq_prefill(ctypes.byref(x), None) == -1
+    nb = sq.sq_prefill_workspace(1, 5000, 4, 128, 128, torch.bfloat16, 1)
+    assert nb > 0
+    for ws, size in ((None, nb), (A, 1 << 16), (A + 16, nb)):
+        x = sq.SqPrefillDesc(**d, workspace=ws, workspace_bytes=size)
+        assert sq._lib.sq_prefill(ctypes.byref(x), None) == -1
     assert sq.sq_prefill_workspace(1, 10, 1, 6, 128, torch.bfloat16) == 0
     with pytest.raises(TypeError):
         sq.sq_prefill_workspace(1, 10, 1, 64, 128, torch.float16)
