@@ -430,7 +430,8 @@ __device__ __forceinline__ void put_P(unsigned char (&P)[2][6 * 1024], const Sid
     planes<2>(y.p[0], y.p[1], pl);
 #pragma unroll
     for (int n = 0; n < 2; n++)
-        *reinterpret_cast<u32x4 *>(P[n] + frag_of(mt, ks) * 1024 + lane * 16) = __builtin_bit_cast(u32x4, pl[n]);
+        *reinterpret_cast<u32x4 *>(&P[0][0] + lane * 16 + (6 * n + frag_of(mt, ks)) * 1024) =
+            __builtin_bit_cast(u32x4, pl[n]);
 }
 
 // A fragment of -N (N_ij = D_ij k_i.k_j, i in the second half, j in the first),
@@ -448,7 +449,8 @@ __device__ __forceinline__ void put_N(unsigned char (&T)[3][6 * 1024], const Sid
     planes<3>(y.p[0], y.p[1], pl);
 #pragma unroll
     for (int n = 0; n < 3; n++)
-        *reinterpret_cast<u32x4 *>(T[n] + frag_of(mt, 0) * 1024 + lane * 16) = __builtin_bit_cast(u32x4, pl[n]);
+        *reinterpret_cast<u32x4 *>(&T[0][0] + lane * 16 + (6 * n + frag_of(mt, 0)) * 1024) =
+            __builtin_bit_cast(u32x4, pl[n]);
 }
 
 // T_a and T_b of one chunk as three planes, by one wave.  kf[j][x]: keys
@@ -494,6 +496,7 @@ __device__ __forceinline__ void forward(const float (&m)[16], float (&x)[16], in
 __device__ __forceinline__ void make_T(unsigned char (&T)[3][6 * 1024], float (&A)[2][kH * kLD], const Side &sd, Gram y,
                                        int lane, int g, int c)
 {
+    float *Ag = &A[0][0] + 4 * g * kLD + c;
 #pragma unroll
     for (int b = 0; b < 2; b++)
 #pragma unroll
@@ -504,7 +507,7 @@ __device__ __forceinline__ void make_T(unsigned char (&T)[3][6 * 1024], float (&
 #pragma unroll
             for (int r = 0; r < 4; r++) {
                 const float m = bi[r] * __builtin_amdgcn_exp2f((float)(sd.G[32 * b + i0 + r] - Gj)) * y.kk[b][u][r];
-                A[b][(i0 + r) * kLD + j] = i0 + r > j ? m : 0.0f;
+                Ag[b * kH * kLD + (16 * (u > 0) + r) * kLD + 16 * (u > 1)] = i0 + r > j ? m : 0.0f;
             }
         }
     wave_order();
@@ -563,7 +566,8 @@ __device__ __forceinline__ void make_T(unsigned char (&T)[3][6 * 1024], float (&
         planes<3>(v[0], v[1], pl);
 #pragma unroll
         for (int p = 0; p < 3; p++)
-            *reinterpret_cast<u32x4 *>(T[p] + frag_of(mt, b) * 1024 + lane * 16) = __builtin_bit_cast(u32x4, pl[p]);
+            *reinterpret_cast<u32x4 *>(&T[0][0] + lane * 16 + (6 * p + frag_of(mt, b)) * 1024) =
+                __builtin_bit_cast(u32x4, pl[p]);
     }
 }
 
@@ -665,83 +669,101 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
         };
         // In step n the state's waves are at chunk n (or have not begun); chunk n + 1
         // is made ready, and the gates of chunk n + 2.
-        if (role <= 1) {
-            // 0: keys, and N (plain decay: half of P); 1: queries, gates and (delta) half of P.
-            // The wave reads back, as operands, rows that it has written itself.
+        // 64 rows from global to shared memory: row 4 u + g, 16-byte piece c, at
+        // exchanged piece c ^ swz(4 u + g) = c ^ (4 (u / 2 mod 4) + g)
+        int at_w[4], at_own[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            at_w[i] = g * 256 + ((c ^ (4 * i + g)) * 16);
+            at_own[i] = rho * 256 + (((4 * i + g) ^ c) * 16);  // piece 4 i + g of row perm(0, c)
+        }
+        auto load_rows = [&](__amdgpu_buffer_rsrc_t w, int32_t st, u32x4 (&x)[16]) {
+            const int32_t b = here(g * st + c * 16);
+#pragma unroll
+            for (int u = 0; u < 16; u++) x[u] = __builtin_amdgcn_raw_buffer_load_b128(w, b + 4 * u * st, 0, 0);
+        };
+        auto put_rows = [&](unsigned char *dst, const u32x4 (&x)[16]) {
+#pragma unroll
+            for (int u = 0; u < 16; u++) *reinterpret_cast<u32x4 *>(dst + at_w[(u >> 1) & 3] + u * 1024) = x[u];
+            wave_order();
+        };
+        // an operand from rows that this wave has put itself
+        auto own = [&](const unsigned char *dst, int m, bf16x8 (&o)[4]) {
+#pragma unroll
+            for (int x = 0; x < 4; x++) o[x] = lds16(dst + at_own[x] + perm(m, 0) * 256);
+        };
+        if (role == 0) {
+            // keys; N of the delta rule, half of P with a plain decay.  The rows are
+            // loaded a step ahead, which also brings them to the L2 cache for the waves
+            // that load operands from global memory.
+            u32x4 x[16];
+            load_rows(key_window(0), ks2, x);
+            for (int n = -2; n < chunks; n++) {
+                lds_barrier();
+                if (n + 1 < 0 || n + 1 >= chunks) continue;
+                unsigned char *dst = sm.K[(n + 1) & 1];
+                const Side &sd = sm.side[(n + 1) % 3];
+                put_rows(dst, x);
+                if (n + 2 < chunks) load_rows(key_window(n + 2), ks2, x);
+                if constexpr (DELTA) {
+                    Pair y[2];
+#pragma unroll
+                    for (int m = 0; m < 2; m++) y[m].p[0] = y[m].p[1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int x = 0; x < 4; x++) {
+                        bf16x8 e[4];
+#pragma unroll
+                        for (int m = 0; m < 4; m++) e[m] = lds16(dst + at_own[x] + perm(m, 0) * 256);
+#pragma unroll
+                        for (int m = 0; m < 2; m++)
+#pragma unroll
+                            for (int u = 0; u < 2; u++) y[m].p[u] = mma(e[u], e[2 + m], y[m].p[u]);
+                    }
+#pragma unroll
+                    for (int m = 0; m < 2; m++) put_N(sm.T[(n + 1) & 1], sd, 2 + m, y[m], here(lane), here(g), here(c));
+                } else if constexpr (STEP != kWrites) {
+                    bf16x8 e[2][4], i[4];
+                    own(dst, 0, e[0]);
+                    own(dst, 1, e[1]);
+#pragma unroll
+                    for (int m = 0; m < 2; m++) {
+                        rows(query_window(n + 1), qs2, m, i);
+                        put_P(sm.P[(n + 1) & 1], sd, m, 0, products(e, i), lane, g, c);
+                    }
+                }
+            }
+        } else if (role == 1) {
+            // queries and gates; half of P for the delta rule
+            u32x4 x[16];
             float al = 1.0f, bt = 0.0f;
-            constexpr int PROLE = STEP == kWrites ? -1 : DELTA ? 1 : 0;
             auto gates = [&](int n) {
                 const bool in = lane < tokens_of(n);
                 const int64_t i = (first_of(n) + lane) * a.heads + h;
                 al = in ? a.alpha[i] : 1.0f;
                 bt = in ? a.beta[i] : 0.0f;
             };
-            const int32_t st = role == 0 ? ks2 : qs2;
-            if (role == 1) gates(0);
-            // rows of the next chunk, loaded a step ahead (which also brings them to
-            // the L2 cache for the waves that load operands from global memory)
-            u32x4 x[16];
-            auto load_rows = [&](int n) {
-                const auto w = role == 0 ? key_window(n) : query_window(n);
-                const int32_t b = here(g * st + c * 16);
-#pragma unroll
-                for (int u = 0; u < 16; u++) x[u] = __builtin_amdgcn_raw_buffer_load_b128(w, b + 4 * u * st, 0, 0);
-            };
-            const bool brings = STEP != kWrites || role == 0;
-            if (brings) load_rows(0);
+            gates(0);
+            if constexpr (STEP != kWrites) load_rows(query_window(0), qs2, x);
             for (int n = -2; n < chunks; n++) {
                 lds_barrier();
-                if (brings && n + 1 >= 0 && n + 1 < chunks) {
-                    const auto kw = key_window(n + 1), qw = query_window(n + 1);
-                    bf16x8 f[2][4];
-                    if (role == PROLE) {
-#pragma unroll
-                        for (int m = 0; m < 2; m++) {
-                            if (DELTA) rows(kw, ks2, m, f[m]);  // keys, for the queries' wave
-                            else rows(qw, qs2, m, f[m]);        // queries, for the keys' wave
-                        }
-                    }
-                    unsigned char *dst = role == 0 ? sm.K[(n + 1) & 1] : sm.Q[(n + 1) & 1];
-#pragma unroll
-                    for (int u = 0; u < 16; u++) {
-                        const int row = 4 * u + g;
-                        *reinterpret_cast<u32x4 *>(dst + row * 256 + ((c ^ swz(row)) * 16)) = x[u];
-                    }
-                    if (n + 2 < chunks) load_rows(n + 2);
-                    wave_order();
-                    const Side &sd = sm.side[(n + 1) % 3];
-                    auto own = [&](int m, bf16x8 (&o)[4]) {
-#pragma unroll
-                        for (int x = 0; x < 4; x++)
-                            o[x] = lds16(dst + (perm(m, 0) + rho) * 256 + (((4 * x + g) ^ c) * 16));
-                    };
-                    if (role == PROLE && DELTA) {
-#pragma unroll
-                        for (int m = 0; m < 2; m++) {
-                            bf16x8 e[4];
-                            own(m, e);
-                            put_P(sm.P[(n + 1) & 1], sd, m, 0, products(f, e), lane, g, c);
-                        }
-                    } else if (role == PROLE) {
-                        bf16x8 e[2][4];
-                        own(0, e[0]);
-                        own(1, e[1]);
-#pragma unroll
-                        for (int m = 0; m < 2; m++) put_P(sm.P[(n + 1) & 1], sd, m, 0, products(e, f[m]), lane, g, c);
-                    } else if constexpr (DELTA) {
-                        bf16x8 e[2][4], i[4];
-                        own(0, e[0]);
-                        own(1, e[1]);
-#pragma unroll
-                        for (int m = 2; m < 4; m++) {
-                            own(m, i);
-                            put_N(sm.T[(n + 1) & 1], sd, m, products(e, i), lane, g, c);
-                        }
-                    }
-                }
-                if (role == 1 && n + 2 < chunks) {
+                if (n + 2 < chunks) {
                     make_side(sm.side[(n + 2) % 3], lane, al, bt);
                     if (n + 3 < chunks) gates(n + 3);
+                }
+                if (STEP == kWrites || n + 1 < 0 || n + 1 >= chunks) continue;
+                unsigned char *dst = sm.Q[(n + 1) & 1];
+                put_rows(dst, x);
+                if (n + 2 < chunks) load_rows(query_window(n + 2), qs2, x);
+                if constexpr (DELTA) {
+                    const auto kw = key_window(n + 1);
+                    bf16x8 f[2][4], e[4];
+                    rows(kw, ks2, 0, f[0]);
+                    rows(kw, ks2, 1, f[1]);
+#pragma unroll
+                    for (int m = 0; m < 2; m++) {
+                        own(dst, m, e);
+                        put_P(sm.P[(n + 1) & 1], sm.side[(n + 1) % 3], m, 0, products(f, e), lane, g, c);
+                    }
                 }
             }
         } else if (!DELTA || role == 2) {
@@ -784,7 +806,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
                             kf[m][x] = __builtin_bit_cast(
                                 bf16x8, __builtin_amdgcn_raw_buffer_load_b128(kw, b + 16 * m * ks2 + 64 * x, 0, 0));
                 }
-                if (now) make_T(sm.T[(n + 1) & 1], sm.A, sm.side[(n + 1) % 3], y, lane, g, c);
+                if (now) make_T(sm.T[(n + 1) & 1], sm.A, sm.side[(n + 1) % 3], y, here(lane), here(g), here(c));
             }
         }
         return;
