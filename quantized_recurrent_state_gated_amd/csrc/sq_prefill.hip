@@ -478,6 +478,14 @@ __device__ __forceinline__ Gram gram(const bf16x8 (&kf)[4][4])
     return y;
 }
 
+// The block above the diagonal of each half, which nothing else writes.
+__device__ __forceinline__ void zero_A(float (&A)[2][kH * kLD], int lane)
+{
+#pragma unroll
+    for (int b = 0; b < 2; b++)
+        *reinterpret_cast<f32x4 *>(&A[b][(lane >> 2) * kLD + 16 + 4 * (lane & 3)]) = f32x4{0, 0, 0, 0};
+}
+
 // x_i = [i == c] + sum_{l < i} m_l(lane i) x_l, i = I .. 15
 template <int I>
 __device__ __forceinline__ void forward(const float (&m)[16], float (&x)[16], int c)
@@ -554,13 +562,12 @@ __device__ __forceinline__ void make_T(unsigned char (&T)[3][6 * 1024], float (&
 #pragma unroll
     for (int mt = 0; mt < 4; mt++) {
         const int b = mt >> 1, row = perm(mt & 1, c), col = 8 * g;
-        f32x4 v[2];
+        f32x4 v[2];  // (zero above the diagonal: the inverses' own zeros, and the block that zero_A cleared)
 #pragma unroll
         for (int u = 0; u < 2; u++) {
             v[u] = *reinterpret_cast<const f32x4 *>(A[b] + row * kLD + col + 4 * u);
             const f32x4 bb = *reinterpret_cast<const f32x4 *>(&sd.be[32 * b + col + 4 * u]);
-#pragma unroll
-            for (int e = 0; e < 4; e++) v[u][e] = row >= col + 4 * u + e ? v[u][e] * bb[e] : 0.0f;
+            v[u] *= bb;
         }
         bf16x8 pl[3];
         planes<3>(v[0], v[1], pl);
@@ -791,6 +798,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
             // T takes longest: its keys are loaded a step ahead, and it goes first
             __builtin_amdgcn_s_setprio(2);
             bf16x8 kf[4][4];
+            zero_A(sm.A, lane);
             for (int n = -2; n < chunks; n++) {
                 lds_barrier();
                 const bool now = n + 1 >= 0 && n + 1 < chunks;
