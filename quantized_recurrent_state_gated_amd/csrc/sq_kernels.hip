@@ -34,7 +34,8 @@
 // o_j = alpha y_j + beta (q.k) v_j.  Template mode kDecay.  FP32 and BF16
 // states take S' with each product and the sum rounded by itself
 // (decay_write): any evaluation of the formula as written gives those bits,
-// where a fused multiply-add moves about one BF16 rounding in 2^15.
+// where a fused multiply-add moves about one BF16 rounding in 2^15.  70 x 576
+// BF16 states step in 496 us (5.4 TB/s), like the delta step bound by HBM.
 #include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
 #include <mutex>

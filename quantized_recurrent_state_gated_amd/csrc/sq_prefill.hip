@@ -603,6 +603,13 @@ __device__ __forceinline__ int nth_longest(const PrefillArgs &a, int n, int lane
 // to come.  One barrier a chunk.  Inputs are read once, and no intermediate
 // leaves the CU.
 //
+// What bounds it.  8 ragged sequences x 48 heads up to 4,096 tokens take 504 us,
+// which is the longest sequence's 64 steps of 15,500 cycles: 0.5 of the bytes'
+// time at the card's copy rate.  Per step (cycles, whole heads, delta) the state's
+// waves work 7,400, of which the matrix instructions are 5,800, and the four waves
+// beside them 8,700 to 11,900, the longest being T's chain of dependent
+// instructions.
+//
 // STEP.  kWhole: a workgroup takes a whole sequence.  With a plain decay the
 // state after a segment is a sum, decay x (state before) + (what the segment
 // writes), so long sequences of few heads are cut into segments of a.seg chunks:
@@ -1061,8 +1068,10 @@ hipError_t chunks_t(const PrefillArgs &a, int64_t units, hipStream_t st)
 
 // How a plain decay's sequences are cut: chunks per segment (0: not), and the
 // number of segment records.  Worth it while the heads of all sequences leave
-// CUs idle and there is something to cut (48 heads x 16 Ki tokens 330 us against
-// 700 uncut); the segments then fill the 256 CUs once.
+// CUs idle and there is something to cut; the segments then fill the 256 CUs once
+// (48 heads x 16 Ki tokens 426 us against 768 uncut, 64 heads x 4,096 tokens 136
+// against 186, 64 heads x 2,048 tokens 93.5 against 93.8; 96 heads x 4,096 tokens 228
+// against 213).
 struct Cut {
     int32_t seg;
     int64_t records;
@@ -1097,9 +1106,9 @@ hipError_t chunked(const PrefillArgs &a, hipStream_t st)
     }
     // One workgroup fits a CU.  While the halves of all heads fit the 256 CUs
     // together, two workgroups a head are faster (a step of fewer columns: delta,
-    // 96 heads x 4,096 tokens 310 us against 421, 48 heads 290 against 374; quarters
-    // 578 and 298); above that, whole heads, whose common work is done once
-    // (144 heads 431 us against 599, 192 heads 453 against 609).
+    // 96 heads x 4,096 tokens 329 us against 387, 48 heads 303 against 363); above
+    // that, whole heads, whose common work is done once (144 heads 391 us against
+    // 625, 192 heads 414 against 637).
     return (int64_t)a.n_seq * a.heads <= 128 ? chunks_t<DELTA, 4, kWhole>(a, a.n_seq, st)
                                              : chunks_t<DELTA, 8, kWhole>(a, a.n_seq, st);
 }
@@ -1119,8 +1128,9 @@ bool chunk_aligned(const PrefillArgs &a)
 
 bool takes_chunks(const PrefillArgs &a, bool bf16)
 {
-    // A few tokens a sequence go faster one by one than as a padded chunk (768 heads,
-    // 8 tokens each: 35 us against 42; 16 tokens 49 against 43).
+    // A few tokens a sequence go faster one by one than as a padded chunk (delta, 768
+    // heads: 8 tokens each 35.5 us against 40, 12 tokens 41 against 41, 16 tokens 46
+    // against 40; 48 heads: 12 tokens 10.4 against 12.6, 16 tokens 11.5 against 10.7).
     const bool few = a.n_tokens <= 12 * (int64_t)a.n_seq;
     return chunk_shape(a.dk, a.dv, bf16) && chunk_aligned(a) && !few;
 }
