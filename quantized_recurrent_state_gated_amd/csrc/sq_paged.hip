@@ -451,14 +451,31 @@ __global__ __launch_bounds__(256) void k_attend(AttendArgs a)
     const int r = (int)(unit / (unsigned)a.c.heads), h = (int)(unit % (unsigned)a.c.heads);
     const int qt = (int)(rest % (unsigned)a.q_tiles), sp = (int)(rest / (unsigned)a.q_tiles);
 
+    // the queries, and without a window the split's first page ids, are asked for
+    // together with the length: none of the three waits for another
+    const int ps = a.c.page_shift, P = 1 << ps;
+    const int qi = qt * 16 + c;  // this lane's query within the group
+    const bool q_in = qi < a.group;
+    const int64_t hq = (int64_t)h * a.group + qi;
+    R qf[NK];
+    {
+        const T *qp = reinterpret_cast<const T *>(a.q) + (int64_t)r * a.q_stride + hq * D;
+#pragma unroll
+        for (int i = 0; i < NK; i++) {
+            if (q_in) qf[i] = load16<R>(qp + i * TL::KSTEP + g * EL);
+            else qf[i] = R{};
+        }
+    }
+    const int32_t *pages_of = a.table + (int64_t)r * a.table_stride;
+    const int64_t early_at = ((int64_t)sp * a.chunk >> ps) + threadIdx.x;
+    int32_t early = 0;
+    if (a.window == 0 && early_at < a.table_stride) early = pages_of[early_at];
+
     const Span s = span_of(a, r);
     const int32_t begin = s.from + sp * a.chunk;
     const int32_t end = begin + a.chunk < s.len ? begin + a.chunk : s.len;
     if (begin >= s.len && sp > 0) return;
 
-    const int qi = qt * 16 + c;  // this lane's query within the group
-    const bool q_in = qi < a.group;
-    const int64_t hq = (int64_t)h * a.group + qi;
     if (s.splits == 0) {  // no tokens: zeros, and the logarithm of an empty sum
         if (wv == 0 && q_in) {
             T *dst = reinterpret_cast<T *>(a.o) + ((int64_t)r * a.q_heads + hq) * D;
@@ -470,12 +487,11 @@ __global__ __launch_bounds__(256) void k_attend(AttendArgs a)
     }
 
     // the split's page ids; an id outside the cache is kept as -1, its keys are masked
-    const int ps = a.c.page_shift, P = 1 << ps;
     const int32_t p0 = begin >> ps, np = ((end - 1) >> ps) - p0 + 1;
     if (threadIdx.x == 0) any_bad = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < np; i += 256) {
-        int32_t id = a.table[(int64_t)r * a.table_stride + p0 + i];
+        int32_t id = a.window == 0 && i < 256 ? early : pages_of[p0 + i];
         if ((uint32_t)id >= (uint32_t)a.c.n_pages) {
             id = -1;
             any_bad = 1;
@@ -483,15 +499,6 @@ __global__ __launch_bounds__(256) void k_attend(AttendArgs a)
         ids[i] = id;
     }
 
-    R qf[NK];
-    {
-        const T *qp = reinterpret_cast<const T *>(a.q) + (int64_t)r * a.q_stride + hq * D;
-#pragma unroll
-        for (int i = 0; i < NK; i++) {
-            if (q_in) qf[i] = load16<R>(qp + i * TL::KSTEP + g * EL);
-            else qf[i] = R{};
-        }
-    }
     __syncthreads();
     const bool bad = any_bad != 0;
 

@@ -604,8 +604,8 @@ __device__ __forceinline__ int nth_longest(const PrefillArgs &a, int n, int lane
 // leaves the CU.
 //
 // What bounds it.  8 ragged sequences x 48 heads up to 4,096 tokens take 504 us,
-// which is the longest sequence's 64 steps of 15,500 cycles: 0.5 of the bytes'
-// time at the card's copy rate.  Per step (cycles, whole heads, delta) the state's
+// which is the longest sequence's 64 steps of 15,500 cycles, and 2.3 times what
+// the bytes take at the card's copy rate.  Per step (cycles, whole heads, delta) the state's
 // waves work 7,400, of which the matrix instructions are 5,800, and the four waves
 // beside them 8,700 to 11,900, the longest being T's chain of dependent
 // instructions.
