@@ -313,11 +313,11 @@ struct SmemChunk {
     alignas(16) unsigned char K[2][kC * 256];
     alignas(16) unsigned char Q[2][kC * 256];
     alignas(16) unsigned char P[2][2][6 * 1024];  // planes of tril(D q.k), fragments
-    alignas(16) Side side[3];
+    alignas(16) Side side[4];
 };
 struct SmemChunkDelta : SmemChunk {
     alignas(16) unsigned char T[2][3][6 * 1024];  // planes of T_a, -N, T_b, fragments
-    alignas(16) float A[2][kH * kLD];             // scratch of the inversion
+    alignas(16) float A[2][2][kH * kLD];          // the inverses, of two chunks
 };
 
 __device__ __forceinline__ bf16x8 lds16(const unsigned char *p)
@@ -453,7 +453,7 @@ __device__ __forceinline__ void put_N(unsigned char (&T)[3][6 * 1024], const Sid
             __builtin_bit_cast(u32x4, pl[n]);
 }
 
-// T_a and T_b of one chunk as three planes, by one wave.  kf[j][x]: keys
+// The inverses of one chunk's two diagonal halves, by one wave.  kf[j][x]: keys
 // 16 j + c, d = 32 x + 8 g ...  The four 16 x 16 diagonal blocks are inverted at
 // once by forward substitution (a lane per column; stable whatever the keys,
 // where a product of powers of the matrix is not), the block below each pair is
@@ -501,8 +501,7 @@ __device__ __forceinline__ void forward(const float (&m)[16], float (&x)[16], in
     if constexpr (I < 15) forward<I + 1>(m, x, c);
 }
 
-__device__ __forceinline__ void make_T(unsigned char (&T)[3][6 * 1024], float (&A)[2][kH * kLD], const Side &sd, Gram y,
-                                       int lane, int g, int c)
+__device__ __forceinline__ void invert(float (&A)[2][kH * kLD], const Side &sd, Gram y, int g, int c)
 {
     float *Ag = &A[0][0] + 4 * g * kLD + c;
 #pragma unroll
@@ -558,7 +557,12 @@ __device__ __forceinline__ void make_T(unsigned char (&T)[3][6 * 1024], float (&
 #pragma unroll
             for (int r = 0; r < 4; r++) A[b][(16 + 4 * g + r) * kLD + c] = -X[b][r];
     }
-    wave_order();
+}
+
+// The inverses times beta, as three planes.
+__device__ __forceinline__ void put_T(unsigned char (&T)[3][6 * 1024], const float (&A)[2][kH * kLD], const Side &sd,
+                                      int lane, int g, int c)
+{
 #pragma unroll
     for (int mt = 0; mt < 4; mt++) {
         const int b = mt >> 1, row = perm(mt & 1, c), col = 8 * g;
@@ -599,16 +603,16 @@ __device__ __forceinline__ int nth_longest(const PrefillArgs &a, int n, int lane
 // A workgroup walks one (sequence, head, 16 NW columns) chunk by chunk.  NW
 // waves hold 16 columns of the state each and do nothing but chunk n; four more
 // run ahead of them and make what is the same for all columns: they bring keys
-// and queries to shared memory and compute the gates, P, T and N of the chunks
-// to come.  One barrier a chunk.  Inputs are read once, and no intermediate
+// and queries to shared memory and compute P, T and N of chunk n + 1, the
+// inverses of chunk n + 2 and the gates of chunk n + 3.  One barrier a chunk.  Inputs are read once, and no intermediate
 // leaves the CU.
 //
-// What bounds it.  8 ragged sequences x 48 heads up to 4,096 tokens take 504 us,
-// which is the longest sequence's 64 steps of 15,500 cycles, and 2.3 times what
-// the bytes take at the card's copy rate.  Per step (cycles, whole heads, delta) the state's
-// waves work 7,400, of which the matrix instructions are 5,800, and the four waves
-// beside them 8,700 to 11,900, the longest being T's chain of dependent
-// instructions.
+// What bounds it.  8 ragged sequences x 48 heads up to 4,096 tokens take 468 us,
+// which is the longest sequence's 64 steps of 12,800 cycles at 1.9 GHz, and 2.2 times
+// what the bytes take at the card's copy rate.  Per step (cycles, whole heads,
+// delta) the state's waves work 7,700 to 10,800, of which the matrix instructions
+// are 5,800, keys with N and T 10,800, queries with gates and scores 9,500, the
+// other scores 9,700 and the inverses' chain of dependent instructions 12,000.
 //
 // STEP.  kWhole: a workgroup takes a whole sequence.  With a plain decay the
 // state after a segment is a sum, decay x (state before) + (what the segment
@@ -682,7 +686,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
                 f[x] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(w, b + 64 * x, 0, 0));
         };
         // In step n the state's waves are at chunk n (or have not begun); chunk n + 1
-        // is made ready, and the gates of chunk n + 2.
+        // is made ready, the inverses of chunk n + 2 and the gates of chunk n + 3.
         // 64 rows from global to shared memory: row 4 u + g, 16-byte piece c, at
         // exchanged piece c ^ swz(4 u + g) = c ^ (4 (u / 2 mod 4) + g)
         int at_w[4], at_own[4];
@@ -707,16 +711,16 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
             for (int x = 0; x < 4; x++) o[x] = lds16(dst + at_own[x] + perm(m, 0) * 256);
         };
         if (role == 0) {
-            // keys; N of the delta rule, half of P with a plain decay.  The rows are
+            // keys; N and T of the delta rule, half of P with a plain decay.  The rows are
             // loaded a step ahead, which also brings them to the L2 cache for the waves
             // that load operands from global memory.
             u32x4 x[16];
             load_rows(key_window(0), ks2, x);
-            for (int n = -2; n < chunks; n++) {
+            for (int n = -3; n < chunks; n++) {
                 lds_barrier();
                 if (n + 1 < 0 || n + 1 >= chunks) continue;
                 unsigned char *dst = sm.K[(n + 1) & 1];
-                const Side &sd = sm.side[(n + 1) % 3];
+                const Side &sd = sm.side[(n + 1) & 3];
                 put_rows(dst, x);
                 if (n + 2 < chunks) load_rows(key_window(n + 2), ks2, x);
                 if constexpr (DELTA) {
@@ -735,6 +739,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
                     }
 #pragma unroll
                     for (int m = 0; m < 2; m++) put_N(sm.T[(n + 1) & 1], sd, 2 + m, y[m], here(lane), here(g), here(c));
+                    put_T(sm.T[(n + 1) & 1], sm.A[(n + 1) & 1], sd, here(lane), here(g), here(c));
                 } else if constexpr (STEP != kWrites) {
                     bf16x8 e[2][4], i[4];
                     own(dst, 0, e[0]);
@@ -758,11 +763,11 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
             };
             gates(0);
             if constexpr (STEP != kWrites) load_rows(query_window(0), qs2, x);
-            for (int n = -2; n < chunks; n++) {
+            for (int n = -3; n < chunks; n++) {
                 lds_barrier();
-                if (n + 2 < chunks) {
-                    make_side(sm.side[(n + 2) % 3], lane, al, bt);
-                    if (n + 3 < chunks) gates(n + 3);
+                if (n + 3 < chunks) {
+                    make_side(sm.side[(n + 3) & 3], lane, al, bt);
+                    if (n + 4 < chunks) gates(n + 4);
                 }
                 if (STEP == kWrites || n + 1 < 0 || n + 1 >= chunks) continue;
                 unsigned char *dst = sm.Q[(n + 1) & 1];
@@ -776,7 +781,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
 #pragma unroll
                     for (int m = 0; m < 2; m++) {
                         own(dst, m, e);
-                        put_P(sm.P[(n + 1) & 1], sm.side[(n + 1) % 3], m, 0, products(f, e), lane, g, c);
+                        put_P(sm.P[(n + 1) & 1], sm.side[(n + 1) & 3], m, 0, products(f, e), lane, g, c);
                     }
                 }
             }
@@ -785,7 +790,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
             constexpr int N = DELTA ? 2 : 1;
             bf16x8 kf[N][2][4], qf[2][4];
             const int ks0 = DELTA ? 0 : role - 2;
-            for (int n = -2; n < chunks; n++) {
+            for (int n = -3; n < chunks; n++) {
                 lds_barrier();
                 if (n + 1 < 0 || n + 1 >= chunks) continue;
                 const auto kw = key_window(n + 1), qw = query_window(n + 1);
@@ -799,20 +804,23 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
                 for (int z = 0; z < N; z++)
 #pragma unroll
                     for (int m = 0; m < 2; m++)
-                        put_P(sm.P[(n + 1) & 1], sm.side[(n + 1) % 3], 2 + m, ks0 + z, products(kf[z], qf[m]), lane, g, c);
+                        put_P(sm.P[(n + 1) & 1], sm.side[(n + 1) & 3], 2 + m, ks0 + z, products(kf[z], qf[m]), lane, g, c);
             }
         } else if constexpr (DELTA) {
-            // T takes longest: its keys are loaded a step ahead, and it goes first
-            __builtin_amdgcn_s_setprio(2);
+            // The inverses take longest: they are made a chunk earlier than the rest, their
+            // keys loaded a step before that.  (No raised priority: the two state waves of
+            // the same SIMD then fall behind, 490 us against 435 for the longest sequence
+            // of prompts of 384 heads.)
             bf16x8 kf[4][4];
-            zero_A(sm.A, lane);
-            for (int n = -2; n < chunks; n++) {
+            zero_A(sm.A[0], lane);
+            zero_A(sm.A[1], lane);
+            for (int n = -3; n < chunks; n++) {
                 lds_barrier();
-                const bool now = n + 1 >= 0 && n + 1 < chunks;
+                const bool now = n + 2 >= 0 && n + 2 < chunks;
                 Gram y;
                 if (now) y = gram(kf);
-                if (n + 2 < chunks) {
-                    const auto kw = key_window(n + 2);
+                if (n + 3 < chunks) {
+                    const auto kw = key_window(n + 3);
                     const int32_t b = here(c * ks2 + 16 * g);
 #pragma unroll
                     for (int m = 0; m < 4; m++)
@@ -821,7 +829,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
                             kf[m][x] = __builtin_bit_cast(
                                 bf16x8, __builtin_amdgcn_raw_buffer_load_b128(kw, b + 16 * m * ks2 + 64 * x, 0, 0));
                 }
-                if (now) make_T(sm.T[(n + 1) & 1], sm.A, sm.side[(n + 1) % 3], y, here(lane), here(g), here(c));
+                if (now) invert(sm.A[n & 1], sm.side[(n + 2) & 3], y, here(g), here(c));
             }
         }
         return;
@@ -896,11 +904,12 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
         load_v(0);
         lds_barrier();
         lds_barrier();
+        lds_barrier();
     }
     for (int n = 0; n < chunks; n++) {
         lds_barrier();
         const unsigned char *K = sm.K[n & 1], *Q = sm.Q[n & 1];
-        const Side &sd = sm.side[n % 3];
+        const Side &sd = sm.side[n & 3];
         f32x4 W[4];  // V, then V - 2^G K S, then W
 #pragma unroll
         for (int m = 0; m < 4; m++)
@@ -1068,20 +1077,20 @@ hipError_t chunks_t(const PrefillArgs &a, int64_t units, hipStream_t st)
 
 // How a plain decay's sequences are cut: chunks per segment (0: not), and the
 // number of segment records.  Worth it while the heads of all sequences leave
-// CUs idle and there is something to cut; the segments then fill the 256 CUs once
-// (48 heads x 16 Ki tokens 426 us against 768 uncut, 64 heads x 4,096 tokens 136
-// against 186, 64 heads x 2,048 tokens 93.5 against 93.8; 96 heads x 4,096 tokens 228
-// against 213).
+// CUs idle and the sequences are long, 40 chunks on average; the segments then
+// fill the 256 CUs once (48 heads x 16 Ki tokens 429 us against 779 uncut, 64 heads x
+// 4,096 tokens 135 against 167, 96 heads 232 against 218; 64 heads x 2,048 tokens 94
+// against 83).
 struct Cut {
     int32_t seg;
     int64_t records;
 };
-constexpr int32_t kCutHeads = 64, kSegMin = 16;
+constexpr int32_t kCutHeads = 64, kCutMin = 40, kSegMin = 16;
 
 Cut cut_of(int32_t n_seq, int32_t n_tokens, int32_t heads)
 {
     const int64_t sh = (int64_t)n_seq * heads, chunks = ((int64_t)n_tokens + kC - 1) / kC;
-    if (sh > kCutHeads || chunks < 2 * kSegMin) return Cut{0, 0};
+    if (sh > kCutHeads || chunks < (int64_t)kCutMin * n_seq) return Cut{0, 0};
     int64_t seg = (chunks * heads + 255 - sh) / (256 - sh);
     if (seg < kSegMin) seg = kSegMin;
     return Cut{(int32_t)seg, (int64_t)n_tokens / (seg * kC) + n_seq + 1};
@@ -1106,9 +1115,9 @@ hipError_t chunked(const PrefillArgs &a, hipStream_t st)
     }
     // One workgroup fits a CU.  While the halves of all heads fit the 256 CUs
     // together, two workgroups a head are faster (a step of fewer columns: delta,
-    // 96 heads x 4,096 tokens 329 us against 387, 48 heads 303 against 363); above
-    // that, whole heads, whose common work is done once (144 heads 391 us against
-    // 625, 192 heads 414 against 637).
+    // 96 heads x 4,096 tokens 321 us against 360, 48 heads 272 against 335); above
+    // that, whole heads, whose common work is done once (144 heads 356 us against
+    // 562, 192 heads 387 against 578).
     return (int64_t)a.n_seq * a.heads <= 128 ? chunks_t<DELTA, 4, kWhole>(a, a.n_seq, st)
                                              : chunks_t<DELTA, 8, kWhole>(a, a.n_seq, st);
 }
@@ -1129,8 +1138,8 @@ bool chunk_aligned(const PrefillArgs &a)
 bool takes_chunks(const PrefillArgs &a, bool bf16)
 {
     // A few tokens a sequence go faster one by one than as a padded chunk (delta, 768
-    // heads: 8 tokens each 35.5 us against 40, 12 tokens 41 against 41, 16 tokens 46
-    // against 40; 48 heads: 12 tokens 10.4 against 12.6, 16 tokens 11.5 against 10.7).
+    // heads: 8 tokens each 36 us against 43, 12 tokens 41 against 43, 16 tokens 46
+    // against 43; 48 heads: 12 tokens 10.7 against 11.6, 16 tokens 11.1 against 11.5).
     const bool few = a.n_tokens <= 12 * (int64_t)a.n_seq;
     return chunk_shape(a.dk, a.dv, bf16) && chunk_aligned(a) && !few;
 }
@@ -1142,7 +1151,7 @@ uint64_t prefill_workspace(int32_t n_seq, int32_t n_tokens, int32_t heads, int32
 {
     // for every call with at most these sizes: records x heads <= min(n_tokens /
     // (64 kSegMin) heads, 256) + n_seq heads + heads, n_seq heads <= kCutHeads
-    if (!chunk_shape(dk, dv, bf16) || delta || n_tokens < 2 * kSegMin * kC - kC + 1) return 0;
+    if (!chunk_shape(dk, dv, bf16) || delta || ((int64_t)n_tokens + kC - 1) / kC < kCutMin || n_seq < 1) return 0;
     const int64_t by_tokens = (int64_t)n_tokens / (kSegMin * kC) * heads, sh = (int64_t)n_seq * heads;
     return cut_bytes((by_tokens < 256 ? by_tokens : 256) + (sh < kCutHeads ? sh : kCutHeads) +
                      (heads < kCutHeads ? heads : kCutHeads));

@@ -132,7 +132,7 @@ def test_many_heads_and_many_sequences(sq, rule):
     check(sq, make(35, [(i * 5) % 14 for i in range(20)], 3, 1, 128, 128, "bf16"), rule, "bf16")
 
 
-@pytest.mark.parametrize("lens,H", [([5000], 1), ([2100, 1024, 0, 1, 3333], 2), ([1, 1984, 64], 3), ([4097], 48)])
+@pytest.mark.parametrize("lens,H", [([5000], 1), ([9000, 1024, 0, 1, 6000], 2), ([2500, 2581], 3), ([4097], 48)])
 def test_long_plain_decay(sq, lens, H):
     """Sequences that are cut into segments, the state out of place and in place."""
     x = make(len(lens) + H, lens, H, H, 128, 128, "bf16")
