@@ -227,8 +227,8 @@ hipError_t launch_tables(const TableArgs &a, hipStream_t st)
 // multiple of TV), a lane writes that piece of its column at once; the other
 // tokens are written element by element.  Slots outside the cache are skipped.
 // Bound by HBM for prompts: four of 8,191 tokens x 8 heads, d = 128 in bfloat16 take
-// 71 us (269 MB, 3.8 TB/s; 98 us when neighbouring lanes took neighbouring columns
-// instead of neighbouring pieces); 70 single tokens take 3.9 us.
+// 71 to 76 us (269 MB, 3.5 to 3.8 TB/s; 98 us when neighbouring lanes took
+// neighbouring columns instead of neighbouring pieces); 70 single tokens take 3.9 us.
 
 namespace {
 
@@ -354,7 +354,7 @@ hipError_t launch_append(const AppendArgs &a, bool bf16, hipStream_t st)
 // (the kernel waits for memory), and a single rounding would double the error
 // that rounding the output makes anyway.
 // 70 requests of up to 16 Ki tokens, 32 query and 8 key-value heads, d = 128 in
-// bfloat16: 420 us, 5.8 TB/s of keys and values read once.
+// bfloat16: 420 to 433 us, 5.6 to 5.8 TB/s of keys and values read once.
 
 namespace {
 
@@ -469,7 +469,7 @@ __global__ __launch_bounds__(256) void k_attend(AttendArgs a)
     const int32_t *pages_of = a.table + (int64_t)r * a.table_stride;
     const int64_t early_at = ((int64_t)sp * a.chunk >> ps) + threadIdx.x;
     int32_t early = 0;
-    if (a.window == 0 && early_at < a.table_stride) early = pages_of[early_at];
+    if (a.window == 0 && early_at < a.table_stride && early_at << ps < a.max_len) early = pages_of[early_at];
 
     const Span s = span_of(a, r);
     const int32_t begin = s.from + sp * a.chunk;
