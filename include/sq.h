@@ -58,6 +58,9 @@
  *   - A pool lives on the device that was current at sq_pool_alloc.  Calls
  *     that enqueue work on it must be made with that device current (else
  *     SQ_ERR_INVALID, nothing enqueued); sq_pool_free switches to it itself.
+ *     Calls without a pool (sq_prefill, sq_block_tables, sq_kv_append,
+ *     sq_paged_attention) run on the current device, which must be the one
+ *     their buffers and stream belong to; this is not checked.
  *   - A slot must not appear twice in one slot_ids batch: two workgroups would
  *     update the same tile (undefined result).  The step does not check slot
  *     ids on the device; sq_check_slots does, as a separate call, and the

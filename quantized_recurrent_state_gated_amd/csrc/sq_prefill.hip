@@ -604,10 +604,10 @@ __device__ __forceinline__ int nth_longest(const PrefillArgs &a, int n, int lane
 // waves hold 16 columns of the state each and do nothing but chunk n; four more
 // run ahead of them and make what is the same for all columns: they bring keys
 // and queries to shared memory and compute P, T and N of chunk n + 1, the
-// inverses of chunk n + 2 and the gates of chunk n + 3.  One barrier a chunk.  Inputs are read once, and no intermediate
-// leaves the CU.
+// inverses of chunk n + 2 and the gates of chunk n + 3.  One barrier a chunk.
+// Inputs are read once, and no intermediate leaves the CU.
 //
-// What bounds it.  8 ragged sequences x 48 heads up to 4,096 tokens take 468 us,
+// What bounds it.  8 ragged sequences x 48 heads up to 4,096 tokens take 466 us,
 // which is the longest sequence's 64 steps of 12,800 cycles at 1.9 GHz, and 2.2 times
 // what the bytes take at the card's copy rate.  Per step (cycles, whole heads,
 // delta) the state's waves work 7,700 to 10,800, of which the matrix instructions
