@@ -376,15 +376,17 @@ uint64_t sq_paged_attention_workspace(const sq_kv_cache *cache, int32_t n_req, i
  *       q_stride elements apart (a multiple of 16 bytes);
  *   block_table, seq_lens  DEVICE int32, as sq_block_tables writes them;
  *   max_len   HOST upper bound of seq_lens (it sets how the context is split
- *       over workgroups); a longer request is cut to its first max_len tokens;
+ *       over workgroups); a longer request is cut to its first max_len tokens,
+ *       and to the table_stride * page_size tokens of its row (the smaller of the
+ *       two at most 2^30);
  *   o   DEVICE [n_req][n_heads][head_dim] of the cache's type;
  *   lse DEVICE fp32 [n_req][n_heads], or NULL: log sum exp(scale q . k_x).
  * A request without tokens gets o = 0 and lse = -inf.  Table entries outside
  * the cache are read as absent tokens.  Keys and values past seq_lens are not
  * used, whatever they hold.  Sums and the softmax are fp32.  n_req == 0 is a
  * no-op.  Errors: SQ_ERR_INVALID (null or misaligned pointer, bad size,
- * workspace too small), SQ_ERR_UNSUPPORTED (page_size, head_dim, launch grid),
- * SQ_ERR_HIP.  Asynchronous on `stream`; the workspace is in use until the
+ * workspace too small), SQ_ERR_UNSUPPORTED (page_size, head_dim, launch grid, more
+ * than 2^30 tokens), SQ_ERR_HIP.  Asynchronous on `stream`; the workspace is in use until the
  * call's work is done. */
 int sq_paged_attention(const sq_kv_cache *cache, const void *q, int64_t q_stride, int32_t n_req,
                        int32_t n_heads, const int32_t *block_table, int64_t table_stride,

@@ -406,12 +406,10 @@ struct Span {
 __device__ __forceinline__ Span span_of(const AttendArgs &a, int r)
 {
     Span s;
-    int64_t len = a.lens[r];
-    const int64_t room = a.table_stride << a.c.page_shift;
+    int32_t len = a.lens[r];
     if (len > a.max_len) len = a.max_len;
-    if (len > room) len = room;
     if (len < 0) len = 0;
-    s.len = (int32_t)len;
+    s.len = len;
     s.first = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
     s.from = s.first & ~31;  // tiles start on multiples of 32 tokens
     s.splits = (s.len - s.from + a.chunk - 1) / a.chunk;
@@ -469,7 +467,7 @@ __global__ __launch_bounds__(256) void k_attend(AttendArgs a)
     const int32_t *pages_of = a.table + (int64_t)r * a.table_stride;
     const int64_t early_at = ((int64_t)sp * a.chunk >> ps) + threadIdx.x;
     int32_t early = 0;
-    if (a.window == 0 && early_at < a.table_stride && early_at << ps < a.max_len) early = pages_of[early_at];
+    if (a.window == 0 && early_at << ps < a.max_len) early = pages_of[early_at];
 
     const Span s = span_of(a, r);
     const int32_t begin = s.from + sp * a.chunk;

@@ -54,6 +54,7 @@ bool stride_ok(int64_t stride, int64_t row, int32_t dtype)
 int status(hipError_t e) { return e == hipSuccess ? SQ_OK : SQ_ERR_HIP; }
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int32_t kMaxReach = 1 << 30;
 
 bool prefill_shape(int32_t dk, int32_t dv)
 {
@@ -161,7 +162,12 @@ int sq_paged_attention(const sq_kv_cache *cache, const void *q, int64_t q_stride
         !aligned(seq_lens, 4))
         return SQ_ERR_INVALID;
     if (!stride_ok(q_stride, (int64_t)n_heads * cache->head_dim, cache->dtype)) return SQ_ERR_INVALID;
-    const int32_t most = window > 0 && window < max_len ? window : max_len;
+    // no request is longer than its table row; token positions are 32 bits in the
+    // kernels, with room for a split's length past the last
+    const int shift = page_shift(cache->page_size);
+    const int32_t reach = table_stride <= (max_len >> shift) ? (int32_t)(table_stride << shift) : max_len;
+    if (reach > kMaxReach) return SQ_ERR_UNSUPPORTED;
+    const int32_t most = window > 0 && window < reach ? window : reach;
     const Split s = split_of(cache, n_req, n_heads, most);
     const uint64_t need =
         s.splits > 1 ? part_bytes(cache, (uint64_t)n_req * (uint64_t)n_heads * (uint64_t)s.splits) : 0;
@@ -179,7 +185,7 @@ int sq_paged_attention(const sq_kv_cache *cache, const void *q, int64_t q_stride
     a.q_heads = n_heads;
     a.group = n_heads / cache->n_kv_heads;
     a.q_tiles = s.q_tiles;
-    a.max_len = max_len;
+    a.max_len = reach;
     a.window = window;
     a.chunk = s.chunk;
     a.splits = s.splits;

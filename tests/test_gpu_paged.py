@@ -278,6 +278,24 @@ def test_attention_takes_length_limits(sq):
     assert (np.abs(o - wo) <= 2.0 ** -14 * mag + 2.0 ** -8 * np.abs(wo)).all()
 
 
+@pytest.mark.parametrize("dtype,P,window", [("bf16", 16, 0), ("bf16", 64, 70), ("f32", 128, 0)])
+def test_attention_with_any_max_len(sq, dtype, P, window):
+    """The largest max_len: the table's rows bound the lengths, and the workspace."""
+    lens = [1000, 1, 0, 700]
+    k, v, t = cache(20 + P, lens, P, 2, 64, dtype)
+    q = queries(20, 4, 4, 64, dtype)
+    c = sq.SqKvCache(k.cuda(), v.cuda())
+    o, lse = torch.empty(4, 4, 64, dtype=k.dtype, device="cuda"), torch.empty(4, 4, device="cuda")
+    room = sq.sq_paged_attention_workspace(c, 4, 4, t.shape[1] * P)
+    ws = torch.empty(max(room, 16), dtype=torch.uint8, device="cuda")
+    sq.sq_paged_attention(c, q.cuda(), torch.from_numpy(t).cuda(), ints(lens), 2 ** 31 - 1, o, ws[:room],
+                          window=window, lse=lse)
+    wo, wl, mag = ref.attention(q.float().numpy(), k.float().numpy(), v.float().numpy(), t, lens, 0.125, window)
+    lim = 2.0 ** -14 * mag + (2.0 ** -8 * np.abs(wo) if dtype == "bf16" else 0.0)
+    assert (np.abs(o.float().cpu().numpy() - wo) <= lim).all()
+    assert np.array_equal(np.isneginf(lse.cpu().numpy()), np.isneginf(wl))
+
+
 def test_attention_strided_queries_streams_and_graph(sq):
     lens = [400, 30, 1]
     k, v, t = cache(12, lens, 16, 2, 128, "bf16")

@@ -172,3 +172,14 @@ def test_binding_checks(sq, monkeypatch):
                     (dict(workspace=[1]), TypeError), (dict(q=t.to(torch.float16)), TypeError)):
         with pytest.raises(err):
             sq.sq_prefill(**(ok | kw))
+
+
+def test_attention_longer_than_its_positions(sq):
+    """Token positions are 32 bits: what a row can hold decides, not max_len alone."""
+    most = 2 ** 31 - 1
+    args = [ctypes.byref(cache(sq)), A, 256, 1, 4, A, most, A, most, 0.125, 0, A, None, A, 1 << 60, None]
+    assert sq._lib.sq_paged_attention(*args) == -2
+    args[8] = 2 ** 30 + 1
+    assert sq._lib.sq_paged_attention(*args) == -2
+    args[10] = 128  # a window does not shorten the row
+    assert sq._lib.sq_paged_attention(*args) == -2
