@@ -319,8 +319,11 @@ template <typename T>
 void append_any(const AppendArgs &a, hipStream_t st)
 {
     // 64 tokens of bfloat16 fill the lines of a page's columns; few tokens: one
-    // piece's worth per workgroup, for more workgroups
-    if ((int64_t)a.n * a.c.heads >= 16384) append_t<T, sizeof(T) == 2 ? 64 : 32>(a, st);
+    // piece's worth per workgroup, for more workgroups.  Tokens x heads, us with
+    // 8 tokens a workgroup against 64 (fp32: 32): 2,048 tokens x 2 heads 5.5 against 5.6
+    // (5.4, 5.3), 512 x 8 5.0 against 5.5 (4.7, 5.2), 4,096 x 2 8.6 against 6.0 (7.8,
+    // 6.1), 1,024 x 8 7.4 against 5.9 (6.7, 5.8), 64 x 8 3.2 against 5.3 (3.2, 4.6).
+    if ((int64_t)a.n * a.c.heads >= 5120) append_t<T, sizeof(T) == 2 ? 64 : 32>(a, st);
     else append_t<T, 8>(a, st);
 }
 

@@ -139,6 +139,12 @@ def test_append(sq, dtype, P, d, H, n):
     assert torch.equal(kd.cpu(), kc) and torch.equal(vd.cpu(), vc)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P,d,H,n", [(256, 256, 6, 853), (256, 256, 6, 854), (32, 96, 5, 1031), (16, 32, 12, 430)])
+def test_append_around_the_larger_tiles(sq, dtype, P, d, H, n):
+    test_append(sq, dtype, P, d, H, n)
+
+
 # ---------------------------------------------------------------- attention
 
 def cache(seed, lens, P, H, d, dtype, fill=0.0):
