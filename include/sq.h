@@ -383,7 +383,10 @@ uint64_t sq_paged_attention_workspace(const sq_kv_cache *cache, int32_t n_req, i
  *   lse DEVICE fp32 [n_req][n_heads], or NULL: log sum exp(scale q . k_x).
  * A request without tokens gets o = 0 and lse = -inf.  Table entries outside
  * the cache are read as absent tokens.  Keys and values past seq_lens are not
- * used, whatever they hold.  Sums and the softmax are fp32.  n_req == 0 is a
+ * used, whatever they hold.  Sums and the softmax are fp32.  A query or key that
+ * is not finite, or a score past the fp32 range, gives NaN in o and lse of the
+ * heads that meet it, except that scores of -inf beside finite ones weigh
+ * nothing; a value that is not finite makes its column of o not finite.  n_req == 0 is a
  * no-op.  Errors: SQ_ERR_INVALID (null or misaligned pointer, bad size,
  * workspace too small), SQ_ERR_UNSUPPORTED (page_size, head_dim, launch grid, more
  * than 2^30 tokens), SQ_ERR_HIP.  Asynchronous on `stream`; the workspace is in use until the

@@ -353,6 +353,10 @@ hipError_t launch_append(const AppendArgs &a, bool bf16, hipStream_t st)
 // of the 32, and lane group g then holds keys 8 g .. 8 g + 7.  The running
 // maximum and sum are per query, that is per lane; the maximum joins the four
 // lane groups with two exchanges per tile, the sum once at the end.
+// The maximum starts at -inf and is at least the lowest float once a key is seen,
+// so that it says by itself whether any was: a request without keys has a
+// maximum of -inf (zeros, log sum -inf), one whose scores are all -inf a sum of
+// zero under a finite maximum (NaN, like any score that is NaN or +inf).
 // P is split into two bfloat16 (hi + lo): the second product costs nothing
 // (the kernel waits for memory), and a single rounding would double the error
 // that rounding the output makes anyway.
@@ -429,6 +433,20 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t *p, f32x4 x)
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
     const bf16x4 y = __builtin_convertvector(x, bf16x4);
     *reinterpret_cast<uint2 *>(p) = __builtin_bit_cast(uint2, y);
+}
+
+constexpr float kFloatMax = 3.402823466e+38f;
+
+// 1 / L and log sum exp of a row with maximum M and sum L (base 2): no keys at
+// all give 0 and -inf, a sum that is zero or NaN under keys gives NaN
+__device__ __forceinline__ float inverse_sum(float M, float L)
+{
+    return M == -__builtin_inff() ? 0.0f : L > 0.0f ? 1.0f / L : __builtin_nanf("");
+}
+__device__ __forceinline__ float log_sum(float M, float L)
+{
+    if (M == -__builtin_inff()) return M;
+    return L > 0.0f ? (M + __builtin_log2f(L)) * 0.69314718055994531f : __builtin_nanf("");
 }
 
 template <typename T, int D>
@@ -557,7 +575,7 @@ __global__ __launch_bounds__(256) void k_attend(AttendArgs a)
 #pragma unroll
             for (int e = 0; e < 4; e++) t[4 * u + e] = x[u][e] * a.scale_log2;
         const bool edge = base + KEYS > end || base < s.first || bad;
-        uint32_t in = 0xffu;
+        uint32_t in = 0xffu;  // the keys that are there
         if (edge) {
             const int32_t key0 = base + vofs;
             const bool page_bad = bad && key0 < end && ids[(key0 >> ps) - p0] < 0;
@@ -569,9 +587,9 @@ __global__ __launch_bounds__(256) void k_attend(AttendArgs a)
                 if (!ok) t[e] = -__builtin_inff();
             }
         }
-        float mx = t[0];
+        float mx = in ? -kFloatMax : -__builtin_inff();
 #pragma unroll
-        for (int e = 1; e < SUB * 4; e++) mx = fmaxf(mx, t[e]);
+        for (int e = 0; e < SUB * 4; e++) mx = fmaxf(mx, t[e]);
         mx = fmaxf(mx, __shfl_xor(mx, 16));
         mx = fmaxf(mx, __shfl_xor(mx, 32));
         if (__ballot(mx > m)) {
@@ -645,12 +663,11 @@ __global__ __launch_bounds__(256) void k_attend(AttendArgs a)
     for (int i = 0; i < ND; i++) acc[i] += sm_o[0][i][lane] + sm_o[1][i][lane] + sm_o[2][i][lane];
     const int64_t row = (int64_t)r * a.q_heads + hq;
     if (s.splits == 1) {
-        const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;  // every key masked: zeros
+        const float inv = inverse_sum(M, L);
         T *dst = reinterpret_cast<T *>(a.o) + row * D;
 #pragma unroll
         for (int i = 0; i < ND; i++) store4<T>(dst + 16 * i + 4 * g, acc[i] * inv);
-        if (a.lse && g == 0)
-            a.lse[row] = L == 0.0f ? -__builtin_inff() : (M + __builtin_log2f(L)) * 0.69314718055994531f;
+        if (a.lse && g == 0) a.lse[row] = log_sum(M, L);
     } else {
         float *dst = a.part + (row * a.splits + sp) * D;
 #pragma unroll
@@ -713,15 +730,14 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a)
     if (lane == 0) sm_l[wv] = L;
     __syncthreads();
     L = sm_l[0] + sm_l[1] + sm_l[2] + sm_l[3];
-    const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
+    const float inv = inverse_sum(M, L);
     T *dst = reinterpret_cast<T *>(a.o) + row * D;
     for (int d = threadIdx.x; d < D; d += 256) {
         const float y = (sm_o[0][d] + sm_o[1][d] + sm_o[2][d] + sm_o[3][d]) * inv;
         if constexpr (sizeof(T) == 4) dst[d] = y;
         else dst[d] = __builtin_bit_cast(uint16_t, (__bf16)y);
     }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[row] = L == 0.0f ? -__builtin_inff() : (M + __builtin_log2f(L)) * 0.69314718055994531f;
+    if (a.lse && threadIdx.x == 0) a.lse[row] = log_sum(M, L);
 }
 
 template <typename T, int D>
