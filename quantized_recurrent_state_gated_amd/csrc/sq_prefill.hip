@@ -32,7 +32,7 @@ __device__ __forceinline__ uint16_t down<uint16_t>(float x)
     return __builtin_bit_cast(uint16_t, (__bf16)x);
 }
 
-// Tokens [first, last) of sequence s, held inside [0, n_tokens) whatever cu says.
+// Tokens [first, last) of sequence s, 0 <= first <= last <= n_tokens whatever cu says.
 struct Seq {
     int32_t first, last;
 };
@@ -41,6 +41,7 @@ __device__ __forceinline__ Seq seq_of(const PrefillArgs &a, int s)
 {
     Seq r{a.cu[s], a.cu[s + 1]};
     if (r.first < 0) r.first = 0;
+    if (r.first > a.n_tokens) r.first = a.n_tokens;
     if (r.last > a.n_tokens) r.last = a.n_tokens;
     if (r.last < r.first) r.last = r.first;
     return r;
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(256) void k_prefill_tokens(PrefillArgs a)
     const int bx = t >> 4, bl = t & 15;
     float nq[NQ], nk[NQ], nv[NV], na = 0.0f, nb = 0.0f;
     auto bring = [&](int32_t t0) {
-        const int64_t tok = t0 + bx;
+        const int64_t tok = (int64_t)t0 + bx;
         if (tok >= sr.last) return;
 #pragma unroll
         for (int i = 0; i < NQ; i++) {
