@@ -254,7 +254,7 @@ typedef enum {
 
 typedef struct {
     int32_t n_seq;             /* sequences, >= 0 */
-    int32_t n_tokens;          /* packed tokens of all sequences, >= 0 */
+    int32_t n_tokens;          /* packed tokens of all sequences, 0 to 2^31 - 65 */
     int32_t n_heads;           /* value (and state) heads, >= 1 */
     int32_t n_k_heads;         /* query/key heads, a divisor of n_heads: head h
                                   reads query/key head h / (n_heads / n_k_heads) */
@@ -295,7 +295,7 @@ uint64_t sq_prefill_workspace(int32_t n_seq, int32_t n_tokens, int32_t n_heads, 
  * they reach the outputs of their own sequence only, but in the chunked kernel
  * also those of earlier tokens of the same 64.  Errors: SQ_ERR_INVALID (null
  * or misaligned pointer, bad size, stride or enum, workspace too small),
- * SQ_ERR_UNSUPPORTED (d_k or d_v, or more tiles than one launch grid),
+ * SQ_ERR_UNSUPPORTED (d_k or d_v, n_tokens, or more tiles than one launch grid),
  * SQ_ERR_HIP. */
 int sq_prefill(const sq_prefill_desc *desc, void *stream);
 

@@ -55,6 +55,7 @@ int status(hipError_t e) { return e == hipSuccess ? SQ_OK : SQ_ERR_HIP; }
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
 constexpr int32_t kMaxReach = 1 << 30;
+constexpr int32_t kMaxTokens = 0x7fffffff - 64;  // the kernels step up to 64 tokens past the last in 32 bits
 
 bool prefill_shape(int32_t dk, int32_t dv)
 {
@@ -217,7 +218,7 @@ int sq_prefill(const sq_prefill_desc *desc, void *stream)
     if (!prefill_sizes(d.n_seq, d.n_tokens, d.n_heads, d.dtype, d.rule) || d.n_k_heads < 1 ||
         d.n_heads % d.n_k_heads != 0)
         return SQ_ERR_INVALID;
-    if (!prefill_shape(d.d_k, d.d_v)) return SQ_ERR_UNSUPPORTED;
+    if (!prefill_shape(d.d_k, d.d_v) || d.n_tokens > kMaxTokens) return SQ_ERR_UNSUPPORTED;
     if (d.n_seq == 0) return SQ_OK;
     if (!d.cu_seqlens || !aligned(d.cu_seqlens, 4)) return SQ_ERR_INVALID;
     if (d.n_tokens > 0) {
