@@ -10,6 +10,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "sq_grid.h"
 #include "sq_paged.h"
 
 namespace sqk {
@@ -308,32 +309,32 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a)
 }
 
 template <typename T, int TT>
-void append_t(const AppendArgs &a, hipStream_t st)
+hipError_t append_t(const AppendArgs &a, hipStream_t st)
 {
-    const unsigned grid = (unsigned)(((int64_t)a.n + TT - 1) / TT * a.c.heads);
+    const int64_t grid = ((int64_t)a.n + TT - 1) / TT * a.c.heads;
+    if (!grid_fits(grid, 256)) return hipErrorInvalidConfiguration;
     const size_t lds = (size_t)TT * (size_t)(a.c.d + 16 / (int)sizeof(T)) * sizeof(T);
-    hipLaunchKernelGGL((k_append<T, TT>), dim3(grid), dim3(256), lds, st, a);
+    hipLaunchKernelGGL((k_append<T, TT>), dim3((unsigned)grid), dim3(256), lds, st, a);
+    return hipGetLastError();
 }
 
 template <typename T>
-void append_any(const AppendArgs &a, hipStream_t st)
+hipError_t append_any(const AppendArgs &a, hipStream_t st)
 {
     // 64 tokens of bfloat16 fill the lines of a page's columns; few tokens: one
     // piece's worth per workgroup, for more workgroups.  Tokens x heads, us with
     // 8 tokens a workgroup against 64 (fp32: 32): 2,048 tokens x 2 heads 5.5 against 5.6
     // (5.4, 5.3), 512 x 8 5.0 against 5.5 (4.7, 5.2), 4,096 x 2 8.6 against 6.0 (7.8,
     // 6.1), 1,024 x 8 7.4 against 5.9 (6.7, 5.8), 64 x 8 3.2 against 5.3 (3.2, 4.6).
-    if ((int64_t)a.n * a.c.heads >= 5120) append_t<T, sizeof(T) == 2 ? 64 : 32>(a, st);
-    else append_t<T, 8>(a, st);
+    if ((int64_t)a.n * a.c.heads >= 5120) return append_t<T, sizeof(T) == 2 ? 64 : 32>(a, st);
+    return append_t<T, 8>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_append(const AppendArgs &a, bool bf16, hipStream_t st)
 {
-    if (bf16) append_any<uint16_t>(a, st);
-    else append_any<float>(a, st);
-    return hipGetLastError();
+    return bf16 ? append_any<uint16_t>(a, st) : append_any<float>(a, st);
 }
 
 // ---------------------------------------------------------------- decode attention
@@ -744,12 +745,11 @@ template <typename T, int D>
 hipError_t attend_td(const AttendArgs &a, hipStream_t st)
 {
     const int64_t grid = (int64_t)a.n * a.c.heads * a.q_tiles * a.splits;
+    const int64_t rows = (int64_t)a.n * a.q_heads;  // of the join
+    if (!grid_fits(grid, 256) || (a.splits > 1 && !grid_fits(rows, 256))) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((k_attend<T, D>), dim3((unsigned)grid), dim3(256), 0, st, a);
     if (hipError_t e = hipGetLastError()) return e;
-    if (a.splits > 1) {
-        const int64_t rows = (int64_t)a.n * a.q_heads;
-        hipLaunchKernelGGL((k_attend_join<T, D>), dim3((unsigned)rows), dim3(256), 0, st, a);
-    }
+    if (a.splits > 1) hipLaunchKernelGGL((k_attend_join<T, D>), dim3((unsigned)rows), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 

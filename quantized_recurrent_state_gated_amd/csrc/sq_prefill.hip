@@ -9,6 +9,7 @@
 
 #include <type_traits>
 
+#include "sq_grid.h"
 #include "sq_prefill.h"
 
 namespace sqk {
@@ -200,7 +201,9 @@ template <typename T, bool DELTA, int LPC>
 hipError_t tokens_l(const PrefillArgs &a, hipStream_t st)
 {
     constexpr int COLS = 256 / LPC;
-    const unsigned grid = (unsigned)((int64_t)a.n_seq * a.heads * ((a.dv + COLS - 1) / COLS));
+    const int64_t groups = (int64_t)a.n_seq * a.heads * ((a.dv + COLS - 1) / COLS);
+    if (!grid_fits(groups, 256)) return hipErrorInvalidConfiguration;
+    const unsigned grid = (unsigned)groups;
     if (a.dk <= 64)
         hipLaunchKernelGGL((k_prefill_tokens<T, DELTA, LPC, 64 / LPC>), dim3(grid), dim3(256), 0, st, a);
     else if (a.dk <= 128)
@@ -1066,13 +1069,14 @@ __global__ __launch_bounds__(64 * (NW + 4)) void k_prefill_chunks(PrefillArgs a)
 template <bool DELTA, int NW, int STEP>
 hipError_t chunks_t(const PrefillArgs &a, int64_t units, hipStream_t st)
 {
-    const unsigned grid = (unsigned)(units * a.heads * (8 / NW));
+    const int64_t grid = units * a.heads * (8 / NW);
+    if (!grid_fits(grid, 64 * (NW + 4))) return hipErrorInvalidConfiguration;
     const size_t lds = DELTA ? sizeof(SmemChunkDelta) : sizeof(SmemChunk);
     auto kern = k_prefill_chunks<DELTA, NW, STEP>;
     if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
         return e;
-    hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * (NW + 4)), lds, st, a);
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * (NW + 4)), lds, st, a);
     return hipGetLastError();
 }
 

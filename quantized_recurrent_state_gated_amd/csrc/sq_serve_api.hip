@@ -51,7 +51,11 @@ bool stride_ok(int64_t stride, int64_t row, int32_t dtype)
     return stride >= row && stride * elem_bytes(dtype) % 16 == 0;
 }
 
-int status(hipError_t e) { return e == hipSuccess ? SQ_OK : SQ_ERR_HIP; }
+// the launchers refuse a grid that does not fit one launch before they make any HIP call
+int status(hipError_t e)
+{
+    return e == hipSuccess ? SQ_OK : e == hipErrorInvalidConfiguration ? SQ_ERR_UNSUPPORTED : SQ_ERR_HIP;
+}
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
 constexpr int32_t kMaxReach = 1 << 30;
@@ -143,7 +147,7 @@ uint64_t sq_paged_attention_workspace(const sq_kv_cache *cache, int32_t n_req, i
                                       int32_t max_len)
 {
     if (cache_ok(cache) != SQ_OK || n_req < 1 || n_heads < 1 || max_len < 0 ||
-        n_heads % cache->n_kv_heads != 0)
+        n_heads % cache->n_kv_heads != 0 || (int64_t)n_req * n_heads > kMaxGrid)
         return 0;
     return part_bytes(cache, sqk::attend_rows_bound(n_req, cache->n_kv_heads, n_heads, max_len));
 }
@@ -167,7 +171,7 @@ int sq_paged_attention(const sq_kv_cache *cache, const void *q, int64_t q_stride
     // kernels, with room for a split's length past the last
     const int shift = page_shift(cache->page_size);
     const int32_t reach = table_stride <= (max_len >> shift) ? (int32_t)(table_stride << shift) : max_len;
-    if (reach > kMaxReach) return SQ_ERR_UNSUPPORTED;
+    if (reach > kMaxReach || (int64_t)n_req * n_heads > kMaxGrid) return SQ_ERR_UNSUPPORTED;
     const int32_t most = window > 0 && window < reach ? window : reach;
     const Split s = split_of(cache, n_req, n_heads, most);
     const uint64_t need =
