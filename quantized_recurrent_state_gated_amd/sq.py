@@ -358,6 +358,14 @@ def sq_decode_step_linear(pool: SqPool, slot_ids, q, k, v, alpha, beta, o=None, 
 
 # ---------------------------------------------------------------- prompts, paged cache
 
+def _int32(x, where: str, name: str) -> int:
+    """A size that the library takes as 32 bits (ctypes would cut it to them)."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise SqError(SQ_ERR_INVALID, f"{where} ({name} = {x} does not fit 32 bits)")
+    return x
+
+
 def _rows(x, where: str, name: str, dtype, shape) -> int:
     """Check a [tokens][heads][d] tensor whose tokens may lie further apart
     than their elements (a part of a wider buffer); returns that distance."""
@@ -386,7 +394,10 @@ def sq_prefill_workspace(n_seq: int, n_tokens: int, n_heads: int, d_k: int, d_v:
     code = {torch.bfloat16: SQ_BF16, torch.float32: SQ_F32}.get(dtype, dtype)
     if not isinstance(code, int):
         raise TypeError(f"sq_prefill_workspace: dtype must be float32 or bfloat16, got {dtype}")
-    return int(_lib.sq_prefill_workspace(n_seq, n_tokens, n_heads, d_k, d_v, code, rule))
+    sizes = [_int32(x, "sq_prefill_workspace", name) for x, name in (
+        (n_seq, "n_seq"), (n_tokens, "n_tokens"), (n_heads, "n_heads"), (d_k, "d_k"), (d_v, "d_v"),
+        (code, "dtype"), (rule, "rule"))]
+    return int(_lib.sq_prefill_workspace(*sizes))
 
 
 def sq_prefill(q, k, v, alpha, beta, cu_seqlens, o, S=None, S0=None, rule: int = SQ_RULE_DELTA,
@@ -401,7 +412,8 @@ def sq_prefill(q, k, v, alpha, beta, cu_seqlens, o, S=None, S0=None, rule: int =
     code, dt = _dtype_code(q), q.dtype
     N, Hk, dk = q.shape
     H, dv = v.shape[1], v.shape[2]
-    n_seq = int(cu_seqlens.numel()) - 1
+    n_seq, rule = int(cu_seqlens.numel()) - 1, _int32(rule, w, "rule")
+    _int32(N, w, "n_tokens")
     qs = _rows(q, w, "q", dt, (N, Hk, dk))
     ks = _rows(k, w, "k", dt, (N, Hk, dk))
     vs = _rows(v, w, "v", dt, (N, H, dv))
@@ -412,7 +424,7 @@ def sq_prefill(q, k, v, alpha, beta, cu_seqlens, o, S=None, S0=None, rule: int =
     _arg(S, w, "S", (torch.float32,), n_seq * H * dk * dv, optional=True)
     _arg(S0, w, "S0", (torch.float32,), n_seq * H * dk * dv, optional=True)
     ws, nb = _workspace(workspace, w)
-    d = SqPrefillDesc(n_seq, N, H, Hk, dk, dv, code, int(rule), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    d = SqPrefillDesc(n_seq, N, H, Hk, dk, dv, code, rule, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                       qs, ks, vs, _ptr(alpha), _ptr(beta), _ptr(cu_seqlens),
                       None if S0 is None else _ptr(S0), _ptr(o), None if S is None else _ptr(S), ws, nb)
     _check(_lib.sq_prefill(ctypes.byref(d), _stream(stream)), w)
@@ -465,7 +477,7 @@ def sq_block_tables(ctx_lens, new_lens, page_size: int, free_pages, block_table,
     _arg(cu_pages, w, "cu_pages", i32, n + 1)
     _arg(slot_map, w, "slot_map", (torch.int64,), slot_map.numel())
     _arg(result, w, "result", i32, 1)
-    _check(_lib.sq_block_tables(_ptr(ctx_lens), _ptr(new_lens), n, int(page_size), _ptr(free_pages),
+    _check(_lib.sq_block_tables(_ptr(ctx_lens), _ptr(new_lens), n, _int32(page_size, w, "page_size"), _ptr(free_pages),
                                 free_pages.numel(), _ptr(block_table), block_table.shape[1],
                                 _ptr(seq_lens), _ptr(cu_new), _ptr(cu_pages), _ptr(slot_map),
                                 slot_map.numel(), _ptr(result), _stream(stream)), w)
@@ -483,7 +495,9 @@ def sq_kv_append(cache: SqKvCache, k, v, slot_map, stream=None) -> None:
 
 
 def sq_paged_attention_workspace(cache: SqKvCache, n_req: int, n_heads: int, max_len: int) -> int:
-    return int(_lib.sq_paged_attention_workspace(cache.ref, n_req, n_heads, max_len))
+    w = "sq_paged_attention_workspace"
+    return int(_lib.sq_paged_attention_workspace(cache.ref, _int32(n_req, w, "n_req"), _int32(n_heads, w, "n_heads"),
+                                                 _int32(max_len, w, "max_len")))
 
 
 def sq_paged_attention(cache: SqKvCache, q, block_table, seq_lens, max_len: int, o, workspace=None,
@@ -504,6 +518,6 @@ def sq_paged_attention(cache: SqKvCache, q, block_table, seq_lens, max_len: int,
     _arg(lse, w, "lse", (torch.float32,), n * heads, optional=True)
     ws, nb = _workspace(workspace, w)
     _check(_lib.sq_paged_attention(cache.ref, q.data_ptr(), qs, n, heads, block_table.data_ptr(),
-                                   block_table.shape[1], seq_lens.data_ptr(), int(max_len),
-                                   d ** -0.5 if scale is None else float(scale), int(window),
+                                   block_table.shape[1], seq_lens.data_ptr(), _int32(max_len, w, "max_len"),
+                                   d ** -0.5 if scale is None else float(scale), _int32(window, w, "window"),
                                    o.data_ptr(), _ptr(lse), ws, nb, _stream(stream)), w)
