@@ -55,16 +55,20 @@ class HybridLayers:
         nb = sq.sq_paged_attention_workspace(self.cache, n, q_heads, max_len)
         self.attend_ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
 
-    def _admit(self, new_lens, slot_map) -> None:
-        """Pages and slots for the requests' next tokens."""
+    def _admit(self, new_lens, slot_map) -> int:
+        """Pages and slots for the requests' next tokens; returns how many pages
+        they take.  Waits for the result: where pages run out, the call ends here,
+        with states, cache, lengths and free list as they were (the rows' entries
+        past the tokens held are written anew by the next call)."""
         sq.sq_block_tables(self.ctx, new_lens, self.page, self.free, self.table, self.seq, self.cu, self.cu_pages,
                            slot_map, self.result)
+        taken, result = torch.cat([self.cu_pages[-1:], self.result]).tolist()
+        if result:
+            raise RuntimeError(f"sq_block_tables reported {result}")
+        return taken
 
-    def _advance(self) -> None:
+    def _advance(self, taken: int) -> None:
         """The tokens are in: lengths move on, the pages taken leave the list."""
-        taken = int(self.cu_pages[-1])  # a server tracks its free list on the host
-        if int(self.result):
-            raise RuntimeError(f"sq_block_tables reported {int(self.result)}")
         self.free = self.free[taken:].contiguous()
         self.ctx, self.seq = self.seq, self.ctx
 
@@ -74,7 +78,7 @@ class HybridLayers:
         new = torch.tensor(lens, dtype=torch.int32, device="cuda")
         N = sum(lens)
         slot_map = torch.empty(N, dtype=torch.int64, device="cuda")
-        self._admit(new, slot_map)
+        taken = self._admit(new, slot_map)
         o = torch.empty_like(x["v"])
         S = torch.empty(self.n, self.heads, D, D, device="cuda")
         nb = sq.sq_prefill_workspace(self.n, N, self.heads, D, D, self.dtype, self.rule)
@@ -82,7 +86,7 @@ class HybridLayers:
         sq.sq_prefill(x["q"], x["k"], x["v"], x["alpha"], x["beta"], self.cu, o, S=S, rule=self.rule, workspace=ws)
         sq.sq_pool_store(self.pool, self.slots, S)
         sq.sq_kv_append(self.cache, x["ak"], x["av"], slot_map)
-        self._advance()
+        self._advance(taken)
         return o
 
     def token(self, x: dict):
@@ -90,14 +94,14 @@ class HybridLayers:
         queries).  Returns the outputs of both layers."""
         one = torch.ones(self.n, dtype=torch.int32, device="cuda")
         slot_map = torch.empty(self.n, dtype=torch.int64, device="cuda")
-        self._admit(one, slot_map)
+        taken = self._admit(one, slot_map)
         o = torch.empty(self.n, self.heads, D, device="cuda")
         step = sq.sq_decode_step if self.rule == sq.SQ_RULE_DELTA else sq.sq_decode_step_linear
         step(self.pool, self.slots, x["q"], x["k"], x["v"], x["alpha"], x["beta"], o)
         sq.sq_kv_append(self.cache, x["ak"], x["av"], slot_map)
         a = torch.empty_like(x["aq"])
         sq.sq_paged_attention(self.cache, x["aq"], self.table, self.seq, self.max_len, a, self.attend_ws)
-        self._advance()
+        self._advance(taken)
         return o, a
 
 
