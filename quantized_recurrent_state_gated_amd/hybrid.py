@@ -6,7 +6,7 @@ fixed-size state per request (here in the quantized pool), the softmax one a
 key-value cache that grows (here in pages).  The loop shows the calls in the
 order a server makes them:
 
-    prompts   sq_block_tables -> sq_prefill -> sq_pool_store
+    prompts   sq_block_tables -> (sq_pool_load) -> sq_prefill -> sq_pool_store
                               -> sq_kv_append
     a token   sq_block_tables -> sq_decode_step (or sq_decode_step_linear)
                               -> sq_kv_append -> sq_paged_attention
@@ -42,6 +42,8 @@ class HybridLayers:
         state = torch.empty(sq.sq_pool_bytes(n, heads, D, D, head_bits), dtype=torch.uint8, device=dev)
         self.pool = sq.sq_pool_alloc(n, heads, D, D, head_bits, ones, ones * scale, state)
         self.slots = torch.arange(n, dtype=torch.int32, device=dev)
+        sq.sq_pool_store(self.pool, self.slots, torch.zeros(n, heads, D, D, device=dev))
+        self.fresh = True  # no request holds a token yet
         # softmax layer: pages for n requests of up to max_len tokens, handed out in any order
         per_row = -(-max_len // page)
         pages = n * per_row
@@ -71,10 +73,13 @@ class HybridLayers:
         """The tokens are in: lengths move on, the pages taken leave the list."""
         self.free = self.free[taken:].contiguous()
         self.ctx, self.seq = self.seq, self.ctx
+        self.fresh = False
 
     def prompts(self, lens, x: dict):
-        """Packed prompts: q, k, v, alpha, beta of the recurrent layer, ak, av of
-        the softmax layer.  Returns the recurrent layer's outputs."""
+        """Packed prompts, or further tokens of requests that hold some: q, k, v,
+        alpha, beta of the recurrent layer, ak, av of the softmax layer.  Returns
+        the recurrent layer's outputs; the softmax layer's prompt tokens only
+        enter the cache (attention over a prompt is not among these calls)."""
         new = torch.tensor(lens, dtype=torch.int32, device="cuda")
         N = sum(lens)
         slot_map = torch.empty(N, dtype=torch.int64, device="cuda")
@@ -83,7 +88,10 @@ class HybridLayers:
         S = torch.empty(self.n, self.heads, D, D, device="cuda")
         nb = sq.sq_prefill_workspace(self.n, N, self.heads, D, D, self.dtype, self.rule)
         ws = torch.empty(nb, dtype=torch.uint8, device="cuda") if nb else None
-        sq.sq_prefill(x["q"], x["k"], x["v"], x["alpha"], x["beta"], self.cu, o, S=S, rule=self.rule, workspace=ws)
+        if not self.fresh:
+            sq.sq_pool_load(self.pool, self.slots, S)
+        sq.sq_prefill(x["q"], x["k"], x["v"], x["alpha"], x["beta"], self.cu, o, S=S, S0=None if self.fresh else S,
+                      rule=self.rule, workspace=ws)
         sq.sq_pool_store(self.pool, self.slots, S)
         sq.sq_kv_append(self.cache, x["ak"], x["av"], slot_map)
         self._advance(taken)
