@@ -291,7 +291,9 @@ uint64_t sq_prefill_workspace(int32_t n_seq, int32_t n_tokens, int32_t n_heads, 
  * undefined outputs.  bfloat16 with d_k = d_v = 128, strides in multiples of
  * 8 elements (at most 2^23), 16-byte aligned q, k, v, o and more than 12 tokens a
  * sequence on average takes the chunked matrix kernel,
- * everything else a token-by-token one.  Non-finite inputs are a caller error:
+ * everything else a token-by-token one.  (So a long prompt goes ten times faster in
+ * a call of its own than among many sequences of a token or two.)  o, S and the
+ * workspace must not overlap the inputs, but S may be S0.  Non-finite inputs are a caller error:
  * they reach the outputs of their own sequence only, but in the chunked kernel
  * also those of earlier tokens of the same 64.  Errors: SQ_ERR_INVALID (null
  * or misaligned pointer, bad size, stride or enum, workspace too small),

@@ -614,9 +614,11 @@ __device__ __forceinline__ int nth_longest(const PrefillArgs &a, int n, int lane
 // inverses of chunk n + 2 and the gates of chunk n + 3.  One barrier a chunk.
 // Inputs are read once, and no intermediate leaves the CU.
 //
-// What bounds it.  8 ragged sequences x 48 heads up to 4,096 tokens take 466 us,
-// which is the longest sequence's 64 steps of 12,800 cycles at 1.9 GHz, and 2.2 times
-// what the bytes take at the card's copy rate.  Per step (cycles, whole heads,
+// What bounds it.  8 ragged sequences x 48 heads up to 4,096 tokens take 465 to 478 us,
+// 2.2 times what the bytes take at the card's copy rate.  The longest sequence's 64
+// steps and the three before them, 12,800 cycles each, are 451 us of it at 1.9 GHz,
+// the rest is the launch and the state's way in and out.  (Launched without a pause the
+// clock falls: 500 to 630 us from the fourth launch on.)  Per step (cycles, whole heads,
 // delta) the state's waves work 7,700 to 10,800, of which the matrix instructions
 // are 5,800, keys with N and T 10,800, queries with gates and scores 9,500, the
 // other scores 9,700 and the inverses' chain of dependent instructions 12,000.
@@ -1086,7 +1088,7 @@ hipError_t chunks_t(const PrefillArgs &a, int64_t units, hipStream_t st)
 // How a plain decay's sequences are cut: chunks per segment (0: not), and the
 // number of segment records.  Worth it while the heads of all sequences leave
 // CUs idle and the sequences are long, 40 chunks on average; the segments then
-// fill the 256 CUs once (48 heads x 16 Ki tokens 429 us against 779 uncut, 64 heads x
+// fill the 256 CUs once (48 heads x 16 Ki tokens from a state 429 us against 779 uncut, 64 heads x
 // 4,096 tokens 135 against 167, 96 heads 232 against 218; 64 heads x 2,048 tokens 94
 // against 83).
 struct Cut {
@@ -1148,6 +1150,9 @@ bool takes_chunks(const PrefillArgs &a, bool bf16)
     // A few tokens a sequence go faster one by one than as a padded chunk (delta, 768
     // heads: 8 tokens each 36 us against 43, 12 tokens 41 against 43, 16 tokens 46
     // against 43; 48 heads: 12 tokens 10.7 against 11.6, 16 tokens 11.1 against 11.5).
+    // A plain decay would have it lower (768 heads: 8 tokens 34 against 30, 12 tokens 39
+    // against 30).  The average is all that the host knows: 400 single tokens with
+    // one sequence of 4,096 take 2,730 us, the long one by itself 285.
     const bool few = a.n_tokens <= 12 * (int64_t)a.n_seq;
     return chunk_shape(a.dk, a.dv, bf16) && chunk_aligned(a) && !few;
 }
