@@ -59,15 +59,15 @@ def algorithmic_bytes_per_step(w, bits) -> int:
 
 # rocprofv3 kernel names of the two timed step instances (bf16 q/k/v; launches
 # of 16,384 tiles or more, two tiles per workgroup)
-STEP_KERNEL = "k_step128x2<unsigned short, true, false, 5>"
-KDA_KERNEL = "k_step128x2<unsigned short, true, true, 5>"
+STEP_KERNEL = "k_step128x2<unsigned short, true, 0, 5>"
+KDA_KERNEL = "k_step128x2<unsigned short, true, 1, 5>"
 
 
 def step_kernel(n_tiles: int, kda: bool = False) -> str:
     """The d = 128 step instance a launch of n_tiles 4/6/8/16-bit tiles takes
     (bf16 q/k/v): two tiles per workgroup from 16,384 tiles, four waves per
     tile from 1,024, else two."""
-    g = "true" if kda else "false"
+    g = 1 if kda else 0  # the gate: one per key channel, one per head
     if n_tiles >= 16384:
         return f"k_step128x2<unsigned short, true, {g}, 5>"
     if n_tiles >= 1024:
