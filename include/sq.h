@@ -85,11 +85,11 @@
  * SWITCHES (environment variables, read once per pool by sq_pool_alloc; a
  * pool keeps what it read)
  *   SQ_CHECK   set and not "0": every call that takes slot ids (store, load,
- *              step, per-channel step, readout) first copies the ids to the
+ *              the steps, readout) first copies the ids to the
  *              host, synchronizing the caller's stream, and returns
  *              SQ_ERR_INVALID before any kernel is enqueued if an id is
  *              outside [0, n_slots) or, for the calls that write the pool
- *              (store and both steps), appears twice.  A debugging aid: it
+ *              (store and the steps), appears twice.  A debugging aid: it
  *              costs a synchronization per call and cannot be used under
  *              graph capture.
  *   SQ_KERNEL  unset, empty or "tuned": d_k = d_v = 128 takes the tuned
@@ -442,8 +442,8 @@ int sq_check_slots(sq_pool *pool, const int32_t *slot_ids, int32_t n_req, int32_
 int sq_check_slots_noalloc(const int32_t *slot_ids, int32_t n_req, int32_t n_slots, int32_t *result,
                            void *stream);
 
-/* Read and clear the pool's sticky device flag.  The step, the per-channel-
- * gate step and the store set it when an updated value (the quotient S'/s for
+/* Read and clear the pool's sticky device flag.  The steps (scalar gate,
+ * per-channel gate, plain decay) and the store set it when an updated value (the quotient S'/s for
  * codes, S' for unquantized heads) is not finite, which only non-finite or
  * huge inputs cause; the stored result then follows the rule above (NaN ->
  * code 0, +-Inf -> +-Q).  Synchronizes `stream` first (host-blocking).
