@@ -158,12 +158,15 @@ __device__ void fill_tables(const TableArgs &a, const int32_t *cn, const int32_t
 {
     const int32_t tokens = cn[a.n], pages = cp[a.n];
     const int P = 1 << a.page_shift;
-    // fresh pages into the rows
-    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < pages; j += (int64_t)gridDim.x * 256) {
+    // fresh pages into the rows; what a row has no room for (lengths past the table
+    // may ask for 2^31 pages) is stepped over at once
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < pages; j += step) {
         const int i = find(cp, a.n, (int32_t)j);
         const Need r = need_of(a, i);
         const int64_t at = r.held + (j - cp[i]);
         if (at < a.stride) a.table[(int64_t)i * a.stride + at] = j < a.n_free ? a.free_pages[j] : -1;
+        else j += (cp[i + 1] - 1 - j) / step * step;
     }
     // slots of the new tokens, and -1 after the last
     for (int64_t b = blockIdx.x; b * kTokensPerBlock < a.capacity; b += gridDim.x) {
