@@ -243,7 +243,8 @@ hipError_t tokens_t(const PrefillArgs &a, hipStream_t st)
 // three planes of 8 bits are the fp32 value to the last bit, two are 16 bits
 // of it.  Whatever feeds the state takes three planes (the state stays an
 // fp32 computation over any length); what only reaches O, which is rounded to
-// bfloat16, takes two.
+// bfloat16, takes two: 2^-16 of the terms that O sums, where the 8 bits of the
+// queries, keys and values themselves leave 2^-9 of them open.
 //
 // Operand order.  A 16 x 16 result holds rows 4 (lane / 16) + r of column
 // lane % 16; an operand wants, per lane, 8 consecutive indexes 8 (lane / 16) + i
@@ -314,7 +315,8 @@ constexpr int kH = 32, kLD = kH + 4;  // halves of the triangular system; rows s
 
 struct Side {
     double G[kC];                            // running sums of log2 alpha
-    float gam[kC], dec[kC], gf[kC], be[kC];  // 2^G, 2^(G_C - G), G, beta
+    float gam[kC], dec[kC], be[kC];          // 2^G, 2^(G_C - G), beta
+    float gh[kC], gl[kC];                    // G as the sum of two floats
 };
 struct SmemChunk {
     alignas(16) unsigned char K[2][kC * 256];
@@ -401,7 +403,8 @@ __device__ __forceinline__ void make_side(Side &sd, int lane, float al, float bt
     sd.G[lane] = x;
     sd.gam[lane] = pow2(x);
     sd.dec[lane] = pow2(last - x);
-    sd.gf[lane] = (float)x;
+    sd.gh[lane] = (float)x;
+    sd.gl[lane] = (float)(x - (double)(float)x);
     sd.be[lane] = bt;
 }
 
@@ -420,18 +423,21 @@ __device__ __forceinline__ Pair products(const bf16x8 (&kf)[2][4], const bf16x8 
     return y;
 }
 
-// A fragment of tril(D_ij q_i.k_j), two planes.
+// A fragment of tril(D_ij q_i.k_j), two planes.  D from G as two floats: gates of
+// zero count 200 each, so a G rounded to one float would be off by up to 2^-11.
 __device__ __forceinline__ void put_P(unsigned char (&P)[2][6 * 1024], const Side &sd, int mt, int ks, Pair y, int lane,
                                       int g, int c)
 {
     const int i = perm(mt, c);
-    const float Gi = sd.gf[i];
+    const float Gi = sd.gh[i], gi = sd.gl[i];
 #pragma unroll
     for (int u = 0; u < 2; u++) {
         const int j0 = perm(2 * ks + u, 4 * g);
-        const f32x4 Gj = *reinterpret_cast<const f32x4 *>(&sd.gf[j0]);
+        const f32x4 Gj = *reinterpret_cast<const f32x4 *>(&sd.gh[j0]);
+        const f32x4 gj = *reinterpret_cast<const f32x4 *>(&sd.gl[j0]);
 #pragma unroll
-        for (int r = 0; r < 4; r++) y.p[u][r] = j0 + r <= i ? y.p[u][r] * __builtin_amdgcn_exp2f(Gi - Gj[r]) : 0.0f;
+        for (int r = 0; r < 4; r++)
+            y.p[u][r] = j0 + r <= i ? y.p[u][r] * __builtin_amdgcn_exp2f((Gi - Gj[r]) + (gi - gj[r])) : 0.0f;
     }
     bf16x8 pl[2];
     planes<2>(y.p[0], y.p[1], pl);
