@@ -1,0 +1,487 @@
+"""Measured cases of the 8-bit paged key-value cache.
+
+Three entry points, reached through ``quantized_recurrent_state_gated_amd.sq``:
+
+  write    sq_kv8_append, sq_kv8_load   quantise new tokens into the cache, and read what they changed back
+  load     sq_kv8_load                  read whole requests back
+  attend   sq_kv8_attention             one new token per request over the cache
+  prompt   sq_kv8_attention             many new tokens per request, causal, over the cache
+
+The cache holds one byte a value and, for every block of 16 token positions and
+head, one fp32 scale for the keys and one for the values.  A block's scale is
+its largest magnitude over 127 (integer codes) or 448 (e4m3 codes); tokens that
+raise it have the codes before them written anew.
+
+Where ``own`` is false, ``run`` computes each in its plain form: elementary
+torch operations in 32 bits (64 where a rounding is decided).
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+BLOCK = 16
+PAGES = (16, 32, 64)
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+TOP = {"int8": 127.0, "e4m3": 448.0}
+LEAST = 2.0 ** -100  # the smallest scale
+
+
+# ------------------------------------------------------------------ cases
+
+def listed():
+    return [
+        # the new tokens of one decode step of the serving batch, contexts up to 16 Ki tokens
+        {"name": "write_decode", "op": "write", "n": 70, "ctx": 16384, "new": 1, "kv": 8, "d": 128, "page": 16,
+         "fmt": "int8", "dtype": "bf16", "spread": 1.0},
+        # four long prompts
+        {"name": "write_prompts", "op": "write", "n": 4, "ctx": 0, "new": 8191, "kv": 8, "d": 128, "page": 64,
+         "fmt": "int8", "dtype": "bf16", "spread": 0.0},
+        # further turns of a few requests, full precision, an odd head size
+        {"name": "write_turns_f32", "op": "write", "n": 5, "ctx": 777, "new": 333, "kv": 3, "d": 96, "page": 32,
+         "fmt": "e4m3", "dtype": "f32", "spread": 0.7},
+        # one short conversation for export
+        {"name": "load_one_f32", "op": "load", "n": 1, "ctx": 201, "kv": 2, "d": 64, "page": 16, "fmt": "e4m3",
+         "dtype": "f32", "spread": 0.0},
+        # eight requests leave for another server
+        {"name": "load_requests", "op": "load", "n": 8, "ctx": 8192, "kv": 8, "d": 128, "page": 16, "fmt": "int8",
+         "dtype": "bf16", "spread": 1.0},
+        # a single short conversation: latency counts
+        {"name": "attend_one", "op": "attend", "n": 1, "ctx": 201, "q": 16, "kv": 2, "d": 128, "page": 16,
+         "fmt": "int8", "dtype": "bf16", "window": 0, "spread": 0.0},
+        # the serving batch, contexts up to 16 Ki tokens
+        {"name": "attend_serving", "op": "attend", "n": 70, "ctx": 16384, "q": 32, "kv": 8, "d": 128, "page": 16,
+         "fmt": "int8", "dtype": "bf16", "window": 0, "spread": 1.0},
+        # few long contexts, full-precision queries, odd group of query heads
+        {"name": "attend_long_f32", "op": "attend", "n": 3, "ctx": 30001, "q": 20, "kv": 4, "d": 64, "page": 32,
+         "fmt": "e4m3", "dtype": "f32", "window": 0, "spread": 0.3},
+        # one long prompt
+        {"name": "prompt_long", "op": "prompt", "n": 1, "ctx": 0, "new": 8192, "q": 32, "kv": 8, "d": 128, "page": 64,
+         "fmt": "int8", "dtype": "bf16", "window": 0, "spread": 0.0},
+        # pieces of six ragged prompts behind the pieces before them
+        {"name": "prompt_chunks", "op": "prompt", "n": 6, "ctx": 6000, "new": 1024, "q": 32, "kv": 8, "d": 128,
+         "page": 16, "fmt": "e4m3", "dtype": "bf16", "window": 0, "spread": 0.8},
+        # a short further turn behind one long document
+        {"name": "prompt_turn", "op": "prompt", "n": 1, "ctx": 60000, "new": 33, "q": 32, "kv": 8, "d": 128,
+         "page": 16, "fmt": "int8", "dtype": "bf16", "window": 0, "spread": 0.0},
+        # a windowed layer in full precision
+        {"name": "prompt_window_f32", "op": "prompt", "n": 3, "ctx": 500, "new": 700, "q": 6, "kv": 2, "d": 64,
+         "page": 32, "fmt": "int8", "dtype": "f32", "window": 256, "spread": 0.6},
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.5)))))))
+
+
+def draw(rng):
+    op = rng.choice(["write", "write", "load", "attend", "attend", "prompt", "prompt", "prompt"])
+    d, kv = rng.choice([64, 96, 128, 128, 256]), rng.randint(1, 8)
+    dtype = rng.choice(["bf16", "bf16", "f32"])
+    c = {"op": op, "kv": kv, "d": d, "page": rng.choice(PAGES), "fmt": rng.choice(["int8", "e4m3"]), "dtype": dtype,
+         "spread": rng.choice([0.0, 0.5, 1.0])}
+    es = 2 if dtype == "bf16" else 4
+    if op == "write":
+        n = _log(rng, 1, 128)
+        most = 32764 * 8 * 128 * 2 // (n * kv * d * es)
+        new = 1 if rng.random() < 0.4 else _log(rng, 1, max(1, min(16384, most)))
+        return c | {"n": n, "ctx": rng.choice([0, _log(rng, 1, 2048)]), "new": new}
+    if op == "load":
+        n = _log(rng, 1, 64)
+        return c | {"n": n, "ctx": _log(rng, 1, max(1, min(16384, 8 * 4096 * 8 * 128 * 2 // (n * kv * d * es))))}
+    if op == "attend":
+        n = _log(rng, 1, 128)
+        ctx = _log(rng, 1, max(1, min(131072, 70 * 8192 * 8 * 128 // (n * kv * d))))
+        return c | {"n": n, "ctx": ctx, "q": kv * rng.randint(1, 16), "window": rng.choice([0, 0, 0, _log(rng, 1, 8192)])}
+    # scores of the plain form: at most 2^31
+    n, G = _log(rng, 1, 16), rng.randint(1, 8)
+    new = _log(rng, 2, 4096)
+    most = 2 ** 31 // (n * kv * G * new * (128 if d <= 128 else d) // 128 * (4 if dtype == "f32" else 1))
+    if most < new:
+        new = max(2, int(math.sqrt(most * new)))
+        most = new
+    ctx = rng.choice([0, _log(rng, 1, max(1, min(60000, most // 2 - new)))])  # without context half of them are seen
+    return c | {"n": n, "ctx": ctx, "new": new, "q": kv * G, "window": rng.choice([0, 0, 0, _log(rng, 1, 2048)])}
+
+
+def _lens(case, key, salt):
+    """Ragged lengths of a case, at most case[key] and one of them that: the same for every seed, so that a
+    case is one amount of work.  spread 0: all equal; 1: down to a single token, the mean about half."""
+    n, most, spread = case["n"], case.get(key, 0), case["spread"]
+    if most <= 1:
+        return [most] * n
+    out = [most - int(spread * (most - 1) * ((i * 0.6180339887 + 0.37 * salt) % 1.0)) for i in range(n)]
+    out[n // 2] = most
+    return out
+
+
+# ------------------------------------------------------------------ inputs
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def _cu(lens):
+    out = [0]
+    for x in lens:
+        out.append(out[-1] + x)
+    return _ints(out)
+
+
+def _tables(lens, page, extra, g):
+    """A fragmented cache: every request's pages lie anywhere in the pool."""
+    need = [-(-x // page) for x in lens]
+    pages = sum(need) + extra
+    perm = torch.randperm(pages, generator=g, device=DEV).to(torch.int32)
+    cols = max(1, max(need))
+    at, col = torch.tensor([0] + need, device=DEV).cumsum(0), torch.arange(cols, device=DEV)
+    idx = (at[:-1, None] + col).clamp(max=pages - 1)
+    held = col < torch.tensor(need, device=DEV)[:, None]
+    return torch.where(held, perm[idx], 0).to(torch.int32).contiguous(), pages
+
+
+def _held(x, over, fmt):
+    """Bytes and scales of values x, blocks over the axes `over`."""
+    s = x.abs().amax(over, keepdim=True) / TOP[fmt]
+    x = x / s
+    if fmt == "int8":
+        return (x.round().clamp_(-127, 127) + 128).to(torch.uint8), s
+    return x.clamp_(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8), s
+
+
+def _cache(c, pages, g):
+    """A cache with contents: values of unit size, and keys some of whose columns are larger."""
+    kv, d, page = c["kv"], c["d"], c["page"]
+    gain = torch.where(torch.rand(kv, 1, 1, d, generator=g, device=DEV) < 0.04, 4.0, 0.9)
+    x = torch.randn(pages, kv, page // BLOCK, BLOCK, d, generator=g, device=DEV)
+    k, sk = _held(x * gain, (3, 4), c["fmt"])
+    del x
+    v, sv = _held(torch.randn(pages, kv, page // BLOCK, d, BLOCK, generator=g, device=DEV), (3, 4), c["fmt"])
+    k = k.view(pages, kv, page, d)
+    scales = torch.stack([sk.view(pages, kv, -1), sv.view(pages, kv, -1)], -1).contiguous()
+    return {"kc": k, "vc": v, "scales": scales, "gain": gain.view(kv, d)}
+
+
+def _handle(s):
+    from quantized_recurrent_state_gated_amd import sq
+    fmt = {"int8": sq.SQ_KV8_INT8, "e4m3": sq.SQ_KV8_E4M3}[s["c"]["fmt"]]
+    return sq.SqKv8Cache(s["kc"], s["vc"], s["scales"], fmt)
+
+
+def prepare(case, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(int(seed) * 1000003 + 29)
+    c = dict(case)
+    op, dt = c["op"], DTYPES[c["dtype"]]
+    ctx, new = _lens(c, "ctx", 1), _lens(c, "new", 2)
+    seq = [a + b for a, b in zip(ctx, new)]
+    table, pages = _tables(seq, c["page"], 3, g)
+    s = {"c": c, "table": table, "ctx": _ints(ctx), "seq": _ints(seq), "most": max(seq)} | _cache(c, pages, g)
+    if op == "write":
+        N, shape = sum(new), (sum(new), c["kv"], c["d"])
+        first = [a // BLOCK * BLOCK for a in ctx]  # the blocks that a call may change begin here
+        s |= {"cu": _cu(new), "first": _ints(first), "back": _cu([a - b for a, b in zip(seq, first)]),
+              "k": (torch.randn(shape, generator=g, device=DEV) * s["gain"]).to(dt),
+              "v": torch.randn(shape, generator=g, device=DEV).to(dt), "N": N}
+        rows = sum(a - b for a, b in zip(seq, first))
+    elif op == "load":
+        s |= {"first": torch.zeros_like(s["ctx"]), "back": _cu(ctx)}
+        rows = sum(ctx)
+    else:
+        N = c["n"] if op == "attend" else sum(new)
+        s |= {"q": torch.randn(N, c["q"], c["d"], generator=g, device=DEV).to(dt),
+              "cu": None if op == "attend" else _cu(new), "m": max(new)}
+    if op in ("write", "load"):
+        s |= {"ko": torch.empty(rows, c["kv"], c["d"], dtype=dt, device=DEV),
+              "vo": torch.empty(rows, c["kv"], c["d"], dtype=dt, device=DEV)}
+    if own:
+        s["cache"] = _handle(s)
+        if "q" in s:
+            from quantized_recurrent_state_gated_amd import sq
+            nb = sq.sq_kv8_attention_workspace(s["cache"], c["n"], s["q"].shape[0], c["q"], s["most"])
+            s |= {"ws": torch.empty(max(nb, 256), dtype=torch.uint8, device=DEV), "o": torch.empty_like(s["q"]),
+                  "lse": torch.empty(s["q"].shape[:2], device=DEV)}
+    return s
+
+
+# ------------------------------------------------------------------ one pass
+
+def run(s):
+    op = s["c"]["op"]
+    if own:
+        return {"write": _own_write, "load": _own_load, "attend": _own_attend, "prompt": _own_attend}[op](s)
+    return {"write": _plain_write, "load": _plain_load, "attend": _plain_attend, "prompt": _plain_prompt}[op](s)
+
+
+def _own_write(s):
+    from quantized_recurrent_state_gated_amd import sq
+    sq.sq_kv8_append(s["cache"], s["k"], s["v"], s["ctx"], s["cu"], s["table"])
+    return _own_load(s) | {"scales": s["scales"]}
+
+
+def _own_load(s):
+    from quantized_recurrent_state_gated_amd import sq
+    sq.sq_kv8_load(s["cache"], s["table"], s["back"], s["ko"], s["vo"], first=s["first"])
+    return {"k": s["ko"], "v": s["vo"]}
+
+
+def _own_attend(s):
+    from quantized_recurrent_state_gated_amd import sq
+    sq.sq_kv8_attention(s["cache"], s["q"], s["table"], s["seq"], s["most"], s["o"], s["ws"], cu_q=s["cu"],
+                        window=s["c"]["window"], lse=s["lse"])
+    return {"o": s["o"], "lse": s["lse"]}
+
+
+def _values(u, fmt):
+    return u.float() - 128.0 if fmt == "int8" else u.view(torch.float8_e4m3fn).float()
+
+
+def _bytes(x, s, fmt):
+    """Bytes of x at scales s.  The quotient is taken in 64 bits: a rounding is decided by it."""
+    y = x.double() / s.double()
+    if fmt == "int8":
+        return (y.round().clamp(-127, 127) + 128).to(torch.uint8)
+    step = torch.exp2((torch.frexp(y).exponent - 1).clamp(min=-6).double() - 3.0)  # between neighbours in e4m3
+    return ((y / step).round() * step).clamp(-448, 448).float().to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def _places(s, cu, start, count):
+    """Page, block, place in the block and request of packed tokens."""
+    page, t = s["c"]["page"], torch.arange(count, device=DEV)
+    req = torch.searchsorted(cu, t, right=True) - 1
+    pos = start[req] + (t - cu[req])
+    return s["table"][req, pos // page].long(), pos % page // BLOCK, pos % BLOCK, req
+
+
+def _plain_write(s):
+    c, heads = s["c"], torch.arange(s["c"]["kv"], device=DEV)
+    fmt, kv, d, per = c["fmt"], c["kv"], c["d"], c["page"] // BLOCK
+    page, blk, at, req = _places(s, s["cu"], s["ctx"], s["N"])
+    key = page * per + blk
+    blocks = s["scales"].shape[0] * per
+    k = s["kc"].view(-1, kv, per, BLOCK, d)
+    # the block that each request's new tokens begin in, and its tokens before them
+    some = s["cu"][1:] > s["cu"][:-1]
+    f = s["ctx"].clamp(max=s["table"].shape[1] * c["page"] - 1)
+    p0 = s["table"].gather(1, (f // c["page"])[:, None].long())[:, 0].long()
+    b0, held = f % c["page"] // BLOCK, torch.where(some, f % BLOCK, 0)
+    scales = s["scales"].permute(0, 2, 1, 3).reshape(blocks, kv, 2)
+    new = torch.zeros_like(scales)
+    for i, x in ((0, s["k"]), (1, s["v"])):
+        a = torch.zeros(blocks, kv, device=DEV).index_reduce_(0, key, x.float().abs().amax(-1), "amax")
+        new[..., i] = (a.double() / TOP[fmt]).float().clamp(min=LEAST)
+    touched = torch.zeros(blocks, dtype=torch.bool, device=DEV)
+    touched[key] = True
+    going_on = torch.zeros_like(touched)
+    going_on[(p0 * per + b0)[held > 0]] = True
+    now = torch.where(touched[:, None, None], torch.where(going_on[:, None, None], torch.maximum(scales, new), new), scales)
+    # the codes before the new ones, where their scale has grown
+    old, grown = scales[p0 * per + b0], now[p0 * per + b0]
+    places = torch.arange(BLOCK, device=DEV)
+    again = (places < held[:, None])[:, None] & (grown > old)[..., 0, None]
+    ck = k[p0[:, None], heads, b0[:, None]]
+    wk = _bytes(_values(ck, fmt) * old[..., 0, None, None], grown[..., 0, None, None], fmt)
+    k[p0[:, None], heads, b0[:, None]] = torch.where(again[..., None], wk, ck)
+    again = (places < held[:, None])[:, None] & (grown > old)[..., 1, None]
+    cv = s["vc"][p0[:, None], heads, b0[:, None]]
+    wv = _bytes(_values(cv, fmt) * old[..., 1, None, None], grown[..., 1, None, None], fmt)
+    s["vc"][p0[:, None], heads, b0[:, None]] = torch.where(again[:, :, None], wv, cv)
+    k[page[:, None], heads, blk[:, None], at[:, None]] = _bytes(s["k"], now[key][..., 0, None], fmt)
+    s["vc"].transpose(-1, -2)[page[:, None], heads, blk[:, None], at[:, None]] = _bytes(s["v"], now[key][..., 1, None], fmt)
+    s["scales"].copy_(now.view(-1, per, kv, 2).permute(0, 2, 1, 3))
+    return _plain_load(s) | {"scales": s["scales"]}
+
+
+def _plain_load(s):
+    c, heads = s["c"], torch.arange(s["c"]["kv"], device=DEV)
+    fmt, per = c["fmt"], c["page"] // BLOCK
+    page, blk, at, _ = _places(s, s["back"], s["first"], s["ko"].shape[0])
+    at = (page[:, None], heads, blk[:, None], at[:, None])
+    sc = s["scales"][at[:3]]
+    k = s["kc"].view(-1, c["kv"], per, BLOCK, c["d"])[at]
+    v = s["vc"].transpose(-1, -2)[at]
+    dt = s["ko"].dtype
+    return {"k": (_values(k, fmt) * sc[..., 0, None]).to(dt), "v": (_values(v, fmt) * sc[..., 1, None]).to(dt)}
+
+
+def _dense(s):
+    """Keys and values [n][kv][L][d] of whole requests."""
+    c, t = s["c"], s["table"].long()
+    n, kv, d = c["n"], c["kv"], c["d"]
+    sc = s["scales"][t]  # [n][pages][kv][blocks][2]
+    k = _values(s["kc"][t], c["fmt"]).view(sc.shape[:-1] + (BLOCK, d)).mul_(sc[..., 0, None, None])
+    v = _values(s["vc"][t], c["fmt"]).mul_(sc[..., 1, None, None]).transpose(-1, -2)
+    return (x.transpose(1, 2).reshape(n, kv, -1, d) for x in (k, v))
+
+
+def _softmax(x):
+    """Of masked scores, in place; rows that see nothing give zeros and -inf."""
+    top = x.amax(-1, keepdim=True)
+    e = x.sub_(top.clamp(min=-3e38)).exp_()
+    tot = e.sum(-1, keepdim=True)
+    return e, tot, torch.where(tot > 0, top + tot.log(), float("-inf"))
+
+
+def _plain_attend(s):
+    c = s["c"]
+    n, kv, d = c["n"], c["kv"], c["d"]
+    K, V = _dense(s)
+    q = s["q"].float().view(n, kv, c["q"] // kv, d)
+    x = torch.matmul(q, K.transpose(-1, -2)) / math.sqrt(d)
+    pos, lens = torch.arange(K.shape[2], device=DEV), s["seq"][:, None]
+    seen = pos < lens
+    if c["window"]:
+        seen &= pos >= lens - c["window"]
+    e, tot, lse = _softmax(x.masked_fill_(~seen[:, None, None], float("-inf")))
+    o = torch.matmul(e, V) / tot
+    return {"o": o.reshape(n, c["q"], d).to(s["q"].dtype), "lse": lse.reshape(n, c["q"])}
+
+
+def _plain_prompt(s):
+    c, m = s["c"], s["m"]
+    n, kv, d, G = c["n"], c["kv"], c["d"], c["q"] // c["kv"]
+    K, V = _dense(s)
+    L, cu = K.shape[2], s["cu"].long()
+    i = torch.arange(m, device=DEV)
+    there = i < (cu[1:] - cu[:-1])[:, None]
+    q = s["q"][(cu[:-1, None] + i).clamp(max=s["q"].shape[0] - 1)].float()  # [n][m][heads][d], padded
+    q = q.view(n, m, kv, G, d).permute(0, 2, 3, 1, 4).reshape(n, kv, G * m, d)
+    x = torch.matmul(q, K.transpose(-1, -2)).mul_(1.0 / math.sqrt(d)).view(n, kv, G, m, L)
+    own_pos = (s["ctx"][:, None] + i)[..., None]
+    pos = torch.arange(L, device=DEV)
+    seen = pos <= own_pos
+    if c["window"]:
+        seen &= pos > own_pos - c["window"]
+    e, tot, lse = _softmax(x.masked_fill_(~seen[:, None, None], float("-inf")))
+    o = torch.matmul(e.view(n, kv, G * m, L), V).view(n, kv, G, m, d) / tot
+    o = o.permute(0, 3, 1, 2, 4).reshape(n, m, c["q"], d)[there]
+    return {"o": o.to(s["q"].dtype), "lse": lse[..., 0].permute(0, 3, 1, 2).reshape(n, m, c["q"])[there]}
+
+
+# ------------------------------------------------------------------ what a pass cannot do without
+
+def work(case):
+    c = case
+    es = 2 if c["dtype"] == "bf16" else 4
+    ctx, new = _lens(c, "ctx", 1), _lens(c, "new", 2)
+    row, blocks = 2 * c["kv"] * c["d"], lambda tokens: -(-tokens // BLOCK) * c["kv"] * 8
+    if c["op"] == "write":
+        back = sum(a % BLOCK + b for a, b in zip(ctx, new))
+        return {"bytes": (sum(new) + back) * row * (es + 1) + 3 * blocks(back), "flops": 0}
+    if c["op"] == "load":
+        return {"bytes": sum(ctx) * row * (es + 1) + blocks(sum(ctx)), "flops": 0}
+    w = c["window"]
+    if c["op"] == "attend":
+        new = [1] * c["n"]
+        ctx = [x - 1 for x in ctx]
+    # the first query of a request sees ctx + 1 tokens, the last ctx + new; the cache is read from the first's window on
+    seen = sum(a + b - max(0, a + 1 - w if w else 0) for a, b in zip(ctx, new))
+    if w:
+        pairs = sum(sum(min(w, x) for x in range(a + 1, a + b + 1)) for a, b in zip(ctx, new))
+    else:
+        pairs = sum(b * a + b * (b + 1) // 2 for a, b in zip(ctx, new))
+    return {"bytes": seen * row + blocks(seen) + sum(new) * c["q"] * (2 * c["d"] * es + 4), "flops": 4 * pairs * c["q"] * c["d"]}
+
+
+# ------------------------------------------------------------------ in 64 bits
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] in ("attend", "prompt"):
+        return _exact_attention(s)
+    if case["op"] == "write":
+        _exact_write(s)
+    return _exact_load(s) | ({"scales": s["scales"].double()} if case["op"] == "write" else {})
+
+
+def _rounded(y, fmt):
+    """The nearest code value to y, the even one of two."""
+    if fmt == "int8":
+        return torch.round(y).clamp(-127, 127)
+    grid = torch.arange(127, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn).double()  # 0 .. 448, code by code
+    a = y.abs().clamp(max=448.0).contiguous()
+    hi = torch.searchsorted(grid, a).clamp(max=126)
+    lo = (hi - 1).clamp(min=0)
+    up, down = grid[hi] - a, a - grid[lo]
+    i = torch.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    return torch.copysign(grid[i], y)
+
+
+def _as_bytes(v, fmt):
+    return (v + 128).to(torch.uint8) if fmt == "int8" else v.float().to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def _exact_write(s):
+    """Request by request and block by block, as the rule is written."""
+    c, fmt, P = s["c"], s["c"]["fmt"], s["c"]["page"]
+    ctx, cu, table = s["ctx"].tolist(), s["cu"].tolist(), s["table"].tolist()
+    for r in range(c["n"]):
+        end = ctx[r] + cu[r + 1] - cu[r]
+        whole = list(range(-(-ctx[r] // BLOCK) * BLOCK, end - BLOCK + 1, BLOCK))  # blocks of new tokens alone, all at once
+        rest = [b for b in range(ctx[r] // BLOCK * BLOCK, end, BLOCK) if b not in set(whole)]
+        for group in [whole] * bool(whole) + [[b] for b in rest]:
+            a, e = max(group[0], ctx[r]), min(group[-1] + BLOCK, end)
+            pages = torch.tensor([table[r][b // P] for b in group], device=DEV)
+            blks = torch.tensor([b % P // BLOCK for b in group], device=DEV)
+            held, there = a - group[0], (e - a if len(group) == 1 else BLOCK)
+            for i, x, code in ((0, s["k"], s["kc"].view(-1, c["kv"], P // BLOCK, BLOCK, c["d"])),
+                               (1, s["v"], s["vc"].transpose(-1, -2))):
+                x = x[cu[r] + a - ctx[r]:cu[r] + e - ctx[r]].double()
+                x = x.view(len(group), there, c["kv"], c["d"]).transpose(1, 2)
+                new = (x.abs().amax((2, 3)) / TOP[fmt]).float().clamp(min=LEAST)
+                old = s["scales"][pages, :, blks, i]
+                now = torch.maximum(old, new) if held else new
+                w = code[pages, :, blks]  # [group][kv][BLOCK][d]
+                if held:
+                    val = _values(w[:, :, :held], fmt) * old[..., None, None]
+                    val = _as_bytes(_rounded(val.double() / now.double()[..., None, None], fmt), fmt)
+                    w[:, :, :held] = torch.where((now > old)[..., None, None], val, w[:, :, :held])
+                w[:, :, held:held + there] = _as_bytes(_rounded(x / now.double()[..., None, None], fmt), fmt)
+                code[pages, :, blks] = w
+                s["scales"][pages, :, blks, i] = now
+
+
+def _request(s, r, n):
+    """Keys and values [kv][n][d] of a request's first n tokens in 64 bits."""
+    c, t = s["c"], s["table"][r].long()
+    sc = s["scales"][t].double()  # [pages][kv][blocks][2]
+    k = s["kc"][t].reshape(sc.shape[:3] + (BLOCK, c["d"]))
+    v = s["vc"][t].transpose(-1, -2)
+    return [((x.double() - 128 if c["fmt"] == "int8" else x.contiguous().view(torch.float8_e4m3fn).double())
+             * sc[..., i, None, None]).transpose(0, 1).reshape(c["kv"], -1, c["d"])[:, :n] for i, x in ((0, k), (1, v))]
+
+
+def _exact_load(s):
+    first, cu = s["first"].tolist(), s["back"].tolist()
+    out = {"k": [], "v": []}
+    for r in range(s["c"]["n"]):
+        k, v = _request(s, r, first[r] + cu[r + 1] - cu[r])
+        out["k"].append(k[:, first[r]:].transpose(0, 1))
+        out["v"].append(v[:, first[r]:].transpose(0, 1))
+    return {name: torch.cat(x) for name, x in out.items()}
+
+
+def _exact_attention(s):
+    c = s["c"]
+    kv, d, G, w = c["kv"], c["d"], c["q"] // c["kv"], c["window"]
+    seq = s["seq"].tolist()
+    cu = list(range(c["n"] + 1)) if s["cu"] is None else s["cu"].tolist()
+    o = torch.empty(s["q"].shape, dtype=torch.float64, device=DEV)
+    lse = torch.empty(s["q"].shape[:2], dtype=torch.float64, device=DEV)
+    for r, n in enumerate(seq):
+        K, V = _request(s, r, n)
+        for a in range(cu[r], cu[r + 1], 2048):  # some queries at a time
+            b = min(a + 2048, cu[r + 1])
+            own_pos = n - cu[r + 1] + torch.arange(a, b, device=DEV)[:, None]
+            pos = torch.arange(n, device=DEV)
+            hidden = (pos > own_pos) | ((pos <= own_pos - w) if w else False)
+            for h in range(kv):
+                q = s["q"][a:b, h * G:(h + 1) * G].double()
+                x = (q.reshape(-1, d) @ K[h].T).view(b - a, G, n) * d ** -0.5
+                x.masked_fill_(hidden[:, None], float("-inf"))
+                l = torch.logsumexp(x, -1)
+                lse[a:b, h * G:(h + 1) * G] = l
+                o[a:b, h * G:(h + 1) * G] = (x.sub_(l[..., None]).exp_().view(-1, n) @ V[h]).view(b - a, G, d)
+    return {"o": o, "lse": lse}
