@@ -2,10 +2,10 @@
 
 Three entry points, reached through ``quantized_recurrent_state_gated_amd.sq``:
 
-  write    sq_kv8_append, sq_kv8_load   quantise new tokens into the cache, and read what they changed back
-  load     sq_kv8_load                  read whole requests back
-  attend   sq_kv8_attention             one new token per request over the cache
-  prompt   sq_kv8_attention             many new tokens per request, causal, over the cache
+  write    sq_kvq_append, sq_kvq_load   quantise new tokens into the cache, and read what they changed back
+  load     sq_kvq_load                  read whole requests back
+  attend   sq_kvq_attention             one new token per request over the cache
+  prompt   sq_kvq_attention             many new tokens per request, causal, over the cache
 
 The cache holds one byte a value and, for every block of 16 token positions and
 head, one fp32 scale for the keys and one for the values.  A block's scale is
@@ -166,8 +166,8 @@ def _cache(c, pages, g):
 
 def _handle(s):
     from quantized_recurrent_state_gated_amd import sq
-    fmt = {"int8": sq.SQ_KV8_INT8, "e4m3": sq.SQ_KV8_E4M3}[s["c"]["fmt"]]
-    return sq.SqKv8Cache(s["kc"], s["vc"], s["scales"], fmt)
+    fmt = {"int8": sq.SQ_KVQ_INT8, "e4m3": sq.SQ_KVQ_E4M3}[s["c"]["fmt"]]
+    return sq.SqKvqCache(s["kc"], s["vc"], s["scales"], fmt)
 
 
 def prepare(case, seed):
@@ -200,7 +200,7 @@ def prepare(case, seed):
         s["cache"] = _handle(s)
         if "q" in s:
             from quantized_recurrent_state_gated_amd import sq
-            nb = sq.sq_kv8_attention_workspace(s["cache"], c["n"], s["q"].shape[0], c["q"], s["most"])
+            nb = sq.sq_kvq_attention_workspace(s["cache"], c["n"], s["q"].shape[0], c["q"], s["most"])
             s |= {"ws": torch.empty(max(nb, 256), dtype=torch.uint8, device=DEV), "o": torch.empty_like(s["q"]),
                   "lse": torch.empty(s["q"].shape[:2], device=DEV)}
     return s
@@ -217,19 +217,19 @@ def run(s):
 
 def _own_write(s):
     from quantized_recurrent_state_gated_amd import sq
-    sq.sq_kv8_append(s["cache"], s["k"], s["v"], s["ctx"], s["cu"], s["table"])
+    sq.sq_kvq_append(s["cache"], s["k"], s["v"], s["ctx"], s["cu"], s["table"])
     return _own_load(s) | {"scales": s["scales"]}
 
 
 def _own_load(s):
     from quantized_recurrent_state_gated_amd import sq
-    sq.sq_kv8_load(s["cache"], s["table"], s["back"], s["ko"], s["vo"], first=s["first"])
+    sq.sq_kvq_load(s["cache"], s["table"], s["back"], s["ko"], s["vo"], first=s["first"])
     return {"k": s["ko"], "v": s["vo"]}
 
 
 def _own_attend(s):
     from quantized_recurrent_state_gated_amd import sq
-    sq.sq_kv8_attention(s["cache"], s["q"], s["table"], s["seq"], s["most"], s["o"], s["ws"], cu_q=s["cu"],
+    sq.sq_kvq_attention(s["cache"], s["q"], s["table"], s["seq"], s["most"], s["o"], s["ws"], cu_q=s["cu"],
                         window=s["c"]["window"], lse=s["lse"])
     return {"o": s["o"], "lse": s["lse"]}
 
