@@ -59,7 +59,7 @@
  *     that enqueue work on it must be made with that device current (else
  *     SQ_ERR_INVALID, nothing enqueued); sq_pool_free switches to it itself.
  *     Calls without a pool (sq_prefill, sq_block_tables, sq_kv_append,
- *     sq_paged_attention) run on the current device, which must be the one
+ *     sq_paged_attention, sq_kvq_*) run on the current device, which must be the one
  *     their buffers and stream belong to; this is not checked.
  *   - A slot must not appear twice in one slot_ids batch: two workgroups would
  *     update the same tile (undefined result).  The step does not check slot
@@ -397,6 +397,105 @@ int sq_paged_attention(const sq_kv_cache *cache, const void *q, int64_t q_stride
                        int32_t n_heads, const int32_t *block_table, int64_t table_stride,
                        const int32_t *seq_lens, int32_t max_len, float scale, int32_t window,
                        void *o, float *lse, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------- 8-bit paged cache
+ *
+ * The paged cache with one byte a value.  A block is 16 token positions of one
+ * page (places 16 b .. 16 b + 15) and head; its keys share one fp32 scale, its
+ * values another.  FORMAT (public):
+ *     k      [n_pages][n_kv_heads][page_size][head_dim]        bytes
+ *     v      [n_pages][n_kv_heads][page_size / 16][head_dim][16] bytes (values
+ *            transposed inside the block)
+ *     scales [n_pages][n_kv_heads][page_size / 16][2]          fp32: keys, values
+ * A byte u stands for fl32(c s), s the block's scale and
+ *     SQ_KVQ_INT8  c = u - 128, an integer in [-127, 127] (excess form, as the
+ *                  8-bit codes of the pool)
+ *     SQ_KVQ_E4M3  c = the OCP e4m3 number u (no infinities, largest 448)
+ * Requests, pages and block tables are those of the paged cache above
+ * (sq_block_tables).  Pages may hold anything past a request's last token,
+ * scales included. */
+typedef enum { SQ_KVQ_INT8 = 0, SQ_KVQ_E4M3 = 1 } sq_kvq_format;
+
+typedef struct {
+    void *k, *v;         /* DEVICE, 16-byte aligned; borrowed */
+    float *scales;       /* DEVICE, 16-byte aligned; borrowed */
+    int32_t n_pages;     /* >= 1 */
+    int32_t page_size;   /* 16, 32, 64, 128 or 256 tokens */
+    int32_t n_kv_heads;  /* >= 1 */
+    int32_t head_dim;    /* 32, 64, 96, 128, 192 or 256 */
+    int32_t format;      /* sq_kvq_format */
+} sq_kvq_cache;
+
+/* Quantize-and-append: the packed tokens [cu_new[r], cu_new[r + 1]) go to
+ * positions ctx_lens[r] on of request r (DEVICE int32 [n_req + 1] and [n_req]:
+ * ctx_lens as given to sq_block_tables, cu_new and block_table as it writes
+ * them; tokens past cu_new[n_req] are padding).  With Q = 127 or 448 and A the
+ * largest finite magnitude of a block's new values,
+ *     s' = max(fl32(A / Q), 2^-100)
+ * is the scale of a block that held no token; where some were (ctx_lens[r]
+ * inside the block) the scale becomes max(s, s').  Codes are x / s rounded to the
+ * nearest, half to even, decided exactly.  If a scale grows, the codes that were
+ * there are written anew from the values they stand for: each growth moves a
+ * value by at most half a step of the new scale.  NaN is stored as 0, infinities
+ * as the block's largest code.  The result does not depend on how the launch
+ * was cut, but on how tokens were divided over calls.
+ *   k, v  DEVICE [n_tok][n_kv_heads][head_dim] of `dtype` (sq_dtype), 16-byte
+ *         aligned, tokens k_stride / v_stride elements apart (a multiple of 16
+ *         bytes).
+ * Tokens of pages outside the cache or past the table's row are skipped, and so
+ * are requests with a negative length; cu_new is held to [0, n_tok].  A page
+ * that gets tokens must belong to one request of the batch.  n_tok == 0 or n_req
+ * == 0 is a no-op.  `cache` is a HOST struct, read during the call.
+ * Errors: SQ_ERR_INVALID (null or misaligned pointer, bad size, stride or enum),
+ * SQ_ERR_UNSUPPORTED (page_size, head_dim, launch grid), SQ_ERR_HIP.
+ * Asynchronous on `stream`. */
+int sq_kvq_append(const sq_kvq_cache *cache, const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                  int32_t dtype, int32_t n_tok, const int32_t *ctx_lens, const int32_t *cu_new, int32_t n_req,
+                  const int32_t *block_table, int64_t table_stride, void *stream);
+
+/* Read back (export, migration, inspection): row cu[r] + i of k and v (DEVICE
+ * [n_tok][n_kv_heads][head_dim] of `dtype`, written; either may be NULL) receives
+ * position first[r] + i of request r, i < cu[r + 1] - cu[r], as fl32(c s) rounded to
+ * `dtype`.  first: DEVICE int32 [n_req], or NULL for zeros; cu: DEVICE int32
+ * [n_req + 1].  Positions of pages outside the cache, or past the table's row, read
+ * as zeros; rows that cu gives to no request stay as they are.  The cache is not
+ * modified.  Otherwise as sq_kvq_append. */
+int sq_kvq_load(const sq_kvq_cache *cache, const int32_t *first, const int32_t *cu, int32_t n_req,
+                const int32_t *block_table, int64_t table_stride, void *k, void *v, int64_t k_stride,
+                int64_t v_stride, int32_t dtype, int32_t n_tok, void *stream);
+
+/* Bytes of workspace for sq_kvq_attention with at most n_req requests, n_q
+ * queries and max_len tokens, and any window (0 if none, or if an argument is
+ * invalid).  Host only. */
+uint64_t sq_kvq_attention_workspace(const sq_kvq_cache *cache, int32_t n_req, int32_t n_q, int32_t n_heads,
+                                    int32_t max_len);
+
+/* Attention over the 8-bit cache, of one new token per request (cu_q NULL, n_q
+ * == n_req) or of the last cu_q[r + 1] - cu_q[r] tokens of each (cu_q DEVICE int32
+ * [n_req + 1], held to [0, n_q]): prompts, pieces of prompts, single tokens, mixed.
+ * The tokens' own keys and values are appended before.  Query i of m of a request
+ * of L = seq_lens[r] tokens stands at position L - m + i and
+ *     o = sum_x p_x v_x,  p = softmax over x of scale q . k_x
+ * goes over the positions x <= its own, of them the last `window` (0: all).  Query
+ * head h reads key-value head h / (n_heads / n_kv_heads).
+ *   q    DEVICE [n_q][n_heads][head_dim] of `dtype` (sq_dtype), queries q_stride
+ *        elements apart (a multiple of 16 bytes);
+ *   o    DEVICE [n_q][n_heads][head_dim] of `dtype`; rows of no request stay as they are;
+ *   lse  DEVICE fp32 [n_q][n_heads], or NULL: log sum exp(scale q . k_x).
+ * max_len, block_table, table_stride, requests that are longer and entries outside
+ * the cache: as for sq_paged_attention; so are the workspace, queries without
+ * tokens (o = 0, lse = -inf) and queries that are not finite (NaN).  Scores, sums
+ * and the softmax are fp32; the codes are multiplied exactly; a weight is kept to 11 bits
+ * (fp32 outputs: 22) and to 2^-30 of its row's largest.  What the cache holds outside
+ * the positions that a request's queries see is not used.  n_req == 0 or n_q == 0 is
+ * a no-op.  Errors: SQ_ERR_INVALID (null or misaligned pointer, bad size, workspace
+ * too small), SQ_ERR_UNSUPPORTED (page_size, head_dim, launch grid, more than 2^30
+ * tokens or 2^30 - 1 rows of requests or queries x heads), SQ_ERR_HIP.
+ * Asynchronous on `stream`; the workspace is in use until the call's work is done. */
+int sq_kvq_attention(const sq_kvq_cache *cache, const void *q, int64_t q_stride, int32_t dtype, int32_t n_q,
+                     int32_t n_heads, const int32_t *cu_q, int32_t n_req, const int32_t *block_table,
+                     int64_t table_stride, const int32_t *seq_lens, int32_t max_len, float scale, int32_t window,
+                     void *o, float *lse, void *workspace, uint64_t workspace_bytes, void *stream);
 
 /* Readout without update ([P5] 空间维度: the head's output is the query read
  * out of the state): o = S^T q from the stored state (dequantized), for

@@ -7,20 +7,13 @@
 #include <string.h>
 
 #include "../../include/sq.h"
+#include "sq_checks.h"
 #include "sq_paged.h"
 #include "sq_prefill.h"
 
+using namespace sqk;
+
 namespace {
-
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
-
-// log2 of a page size in [16, 256], or -1
-int page_shift(int32_t page)
-{
-    for (int s = 4; s <= 8; s++)
-        if (page == 1 << s) return s;
-    return -1;
-}
 
 int cache_ok(const sq_kv_cache *c)
 {
@@ -43,22 +36,6 @@ sqk::CacheArgs cache_args(const sq_kv_cache *c)
     return a;
 }
 
-int elem_bytes(int32_t dtype) { return dtype == SQ_BF16 ? 2 : 4; }
-
-// a token stride: at least a token's elements, and rows that stay 16-byte aligned
-bool stride_ok(int64_t stride, int64_t row, int32_t dtype)
-{
-    return stride >= row && stride * elem_bytes(dtype) % 16 == 0;
-}
-
-// the launchers refuse a grid that does not fit one launch before they make any HIP call
-int status(hipError_t e)
-{
-    return e == hipSuccess ? SQ_OK : e == hipErrorInvalidConfiguration ? SQ_ERR_UNSUPPORTED : SQ_ERR_HIP;
-}
-
-constexpr int64_t kMaxGrid = 0x7fffffff;
-constexpr int32_t kMaxReach = 1 << 30;
 constexpr int32_t kMaxTokens = 0x7fffffff - 64;  // the kernels step up to 64 tokens past the last in 32 bits
 
 bool prefill_shape(int32_t dk, int32_t dv)

@@ -28,7 +28,9 @@ EXPORTED = ("sq_pool_bytes", "sq_pool_alloc", "sq_pool_free", "sq_pool_tile_offs
             "sq_pool_store", "sq_pool_load", "sq_decode_step", "sq_decode_step_kda", "sq_readout",
             "sq_check_slots", "sq_check_slots_noalloc", "sq_pool_last_device_error",
             "sq_status_string", "sq_decode_step_linear", "sq_prefill", "sq_prefill_workspace",
-            "sq_block_tables", "sq_kv_append", "sq_paged_attention", "sq_paged_attention_workspace")
+            "sq_block_tables", "sq_kv_append", "sq_paged_attention", "sq_paged_attention_workspace",
+            "sq_kvq_append", "sq_kvq_load", "sq_kvq_attention", "sq_kvq_attention_workspace")
+SQ_KVQ_INT8, SQ_KVQ_E4M3 = 0, 1
 SQ_RULE_DELTA, SQ_RULE_LINEAR = 0, 1
 
 
@@ -55,6 +57,12 @@ class SqKvCacheDesc(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class SqKvqCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
 _vp, _i32 = ctypes.c_void_p, ctypes.c_int32
@@ -92,6 +100,17 @@ _lib.sq_paged_attention_workspace.argtypes = [ctypes.POINTER(SqKvCacheDesc), _i3
 _lib.sq_paged_attention.restype = ctypes.c_int
 _lib.sq_paged_attention.argtypes = [ctypes.POINTER(SqKvCacheDesc), _vp, _i64, _i32, _i32, _vp, _i64, _vp,
                                     _i32, ctypes.c_float, _i32, _vp, _vp, _vp, _u64, _vp]
+_lib.sq_kvq_append.restype = ctypes.c_int
+_lib.sq_kvq_append.argtypes = [ctypes.POINTER(SqKvqCacheDesc), _vp, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _i32,
+                               _vp, _i64, _vp]
+_lib.sq_kvq_load.restype = ctypes.c_int
+_lib.sq_kvq_load.argtypes = [ctypes.POINTER(SqKvqCacheDesc), _vp, _vp, _i32, _vp, _i64, _vp, _vp, _i64, _i64, _i32,
+                             _i32, _vp]
+_lib.sq_kvq_attention_workspace.restype = _u64
+_lib.sq_kvq_attention_workspace.argtypes = [ctypes.POINTER(SqKvqCacheDesc), _i32, _i32, _i32, _i32]
+_lib.sq_kvq_attention.restype = ctypes.c_int
+_lib.sq_kvq_attention.argtypes = [ctypes.POINTER(SqKvqCacheDesc), _vp, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _i64,
+                                  _vp, _i32, ctypes.c_float, _i32, _vp, _vp, _vp, _u64, _vp]
 _lib.sq_readout.restype = ctypes.c_int
 _lib.sq_readout.argtypes = [_vp, _vp, _i32, _vp, _i32, _vp, _vp]
 _lib.sq_check_slots.restype = ctypes.c_int
@@ -521,3 +540,100 @@ def sq_paged_attention(cache: SqKvCache, q, block_table, seq_lens, max_len: int,
                                    block_table.shape[1], seq_lens.data_ptr(), _int32(max_len, w, "max_len"),
                                    d ** -0.5 if scale is None else float(scale), _int32(window, w, "window"),
                                    o.data_ptr(), _ptr(lse), ws, nb, _stream(stream)), w)
+
+
+# ---------------------------------------------------------------- 8-bit paged cache
+
+class SqKvqCache:
+    """A paged key-value cache of one byte a value over three tensors: k uint8
+    [n_pages][n_kv_heads][page_size][head_dim], v uint8 [n_pages][n_kv_heads][page_size / 16][head_dim][16],
+    scales fp32 [n_pages][n_kv_heads][page_size / 16][2]; keeps them alive."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, scales: torch.Tensor, format: int = SQ_KVQ_INT8):
+        w, u8 = "SqKvqCache", (torch.uint8,)
+        if k.dim() != 4:
+            raise SqError(SQ_ERR_INVALID, f"{w} (k is [n_pages][n_kv_heads][page_size][head_dim])")
+        pages, heads, page, d = k.shape
+        _arg(k, w, "k", u8, k.numel())
+        _arg(v, w, "v", u8, k.numel())
+        _arg(scales, w, "scales", (torch.float32,), pages * heads * (page // 16) * 2)
+        if tuple(v.shape) != (pages, heads, page // 16, d, 16):
+            raise SqError(SQ_ERR_INVALID, f"{w} (v is [n_pages][n_kv_heads][page_size / 16][head_dim][16])")
+        if tuple(scales.shape) != (pages, heads, page // 16, 2):
+            raise SqError(SQ_ERR_INVALID, f"{w} (scales is [n_pages][n_kv_heads][page_size / 16][2])")
+        if format not in (SQ_KVQ_INT8, SQ_KVQ_E4M3):
+            raise SqError(SQ_ERR_INVALID, f"{w} (format {format})")
+        self.k, self.v, self.scales, self.format = k, v, scales, format
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = pages, page, heads, d
+        self.desc = SqKvqCacheDesc(k.data_ptr(), v.data_ptr(), scales.data_ptr(), pages, page, heads, d, format)
+        self.ref = ctypes.byref(self.desc)
+
+
+def sq_kvq_append(cache: SqKvqCache, k, v, ctx_lens, cu_new, block_table, stream=None) -> None:
+    """Quantize and append: tokens cu_new[r] .. cu_new[r + 1] - 1 of k, v [tokens][n_kv_heads][head_dim]
+    (float32 or bfloat16, tokens may be strided) go to positions ctx_lens[r] on of request r."""
+    w, i32 = "sq_kvq_append", (torch.int32,)
+    n, N, code = int(ctx_lens.numel()), k.shape[0], _dtype_code(k)
+    shape = (N, cache.n_kv_heads, cache.head_dim)
+    ks, vs = _rows(k, w, "k", k.dtype, shape), _rows(v, w, "v", k.dtype, shape)
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise SqError(SQ_ERR_INVALID, f"{w} (block_table is [n_req][stride])")
+    _arg(ctx_lens, w, "ctx_lens", i32, n)
+    _arg(cu_new, w, "cu_new", i32, n + 1)
+    _arg(block_table, w, "block_table", i32, block_table.numel())
+    _check(_lib.sq_kvq_append(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs, code, _int32(N, w, "tokens"),
+                              ctx_lens.data_ptr(), cu_new.data_ptr(), n, block_table.data_ptr(), block_table.shape[1],
+                              _stream(stream)), w)
+
+
+def sq_kvq_load(cache: SqKvqCache, block_table, cu, k=None, v=None, first=None, stream=None) -> None:
+    """Read back: rows cu[r] .. cu[r + 1] - 1 of k and v [tokens][n_kv_heads][head_dim] (float32 or
+    bfloat16, tokens may be strided; either may be None) receive positions first[r] (or 0) on of request r."""
+    w, i32 = "sq_kvq_load", (torch.int32,)
+    if k is None and v is None:
+        raise SqError(SQ_ERR_INVALID, f"{w} (k or v is required)")
+    n, some = int(cu.numel()) - 1, v if k is None else k
+    N, dt, code = some.shape[0], some.dtype, _dtype_code(some)
+    shape = (N, cache.n_kv_heads, cache.head_dim)
+    ks = 0 if k is None else _rows(k, w, "k", dt, shape)
+    vs = 0 if v is None else _rows(v, w, "v", dt, shape)
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise SqError(SQ_ERR_INVALID, f"{w} (block_table is [n_req][stride])")
+    _arg(first, w, "first", i32, n, optional=True)
+    _arg(cu, w, "cu", i32, n + 1)
+    _arg(block_table, w, "block_table", i32, block_table.numel())
+    _check(_lib.sq_kvq_load(cache.ref, _ptr(first), cu.data_ptr(), n, block_table.data_ptr(), block_table.shape[1],
+                            _ptr(k), _ptr(v), ks, vs, code, _int32(N, w, "tokens"), _stream(stream)), w)
+
+
+def sq_kvq_attention_workspace(cache: SqKvqCache, n_req: int, n_q: int, n_heads: int, max_len: int) -> int:
+    w = "sq_kvq_attention_workspace"
+    return int(_lib.sq_kvq_attention_workspace(cache.ref, _int32(n_req, w, "n_req"), _int32(n_q, w, "n_q"),
+                                               _int32(n_heads, w, "n_heads"), _int32(max_len, w, "max_len")))
+
+
+def sq_kvq_attention(cache: SqKvqCache, q, block_table, seq_lens, max_len: int, o, workspace=None, cu_q=None,
+                     scale: float | None = None, window: int = 0, lse=None, stream=None) -> None:
+    """Attention of q [queries][n_heads][head_dim] over the cached tokens: one query per request, or with
+    cu_q the last cu_q[r + 1] - cu_q[r] tokens of each, causal; scale defaults to head_dim ** -0.5, window 0
+    is no window.  `workspace`: sq_kvq_attention_workspace bytes."""
+    w = "sq_kvq_attention"
+    if q.dim() != 3:
+        raise SqError(SQ_ERR_INVALID, f"{w} (q is [queries][n_heads][head_dim])")
+    nq, heads, d = q.shape
+    n, code, dt = int(seq_lens.numel()), _dtype_code(q), q.dtype
+    qs = _rows(q, w, "q", dt, (nq, heads, cache.head_dim))
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise SqError(SQ_ERR_INVALID, f"{w} (block_table is [n_req][stride])")
+    if cu_q is not None:
+        _arg(cu_q, w, "cu_q", (torch.int32,), n + 1)
+        cu_q = _ptr(cu_q)
+    _arg(block_table, w, "block_table", (torch.int32,), block_table.numel())
+    _arg(seq_lens, w, "seq_lens", (torch.int32,), n)
+    _arg(o, w, "o", (dt,), nq * heads * d)
+    _arg(lse, w, "lse", (torch.float32,), nq * heads, optional=True)
+    ws, nb = _workspace(workspace, w)
+    _check(_lib.sq_kvq_attention(cache.ref, q.data_ptr(), qs, code, _int32(nq, w, "queries"), heads, cu_q, n,
+                                 block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
+                                 _int32(max_len, w, "max_len"), d ** -0.5 if scale is None else float(scale),
+                                 _int32(window, w, "window"), o.data_ptr(), _ptr(lse), ws, nb, _stream(stream)), w)
