@@ -482,9 +482,10 @@ uint64_t sq_kvq_attention_workspace(const sq_kvq_cache *cache, int32_t n_req, in
  *        elements apart (a multiple of 16 bytes);
  *   o    DEVICE [n_q][n_heads][head_dim] of `dtype`; rows of no request stay as they are;
  *   lse  DEVICE fp32 [n_q][n_heads], or NULL: log sum exp(scale q . k_x).
- * max_len, block_table, table_stride, requests that are longer and entries outside
- * the cache: as for sq_paged_attention; so are the workspace, queries without
- * tokens (o = 0, lse = -inf) and queries that are not finite (NaN).  Scores, sums
+ * max_len is a HOST upper bound of seq_lens, as for sq_paged_attention: positions
+ * from max_len on, or past the table's row, are not seen (queries keep their own).
+ * block_table, entries outside the cache and the workspace are as there; so are queries
+ * without tokens (o = 0, lse = -inf) and queries that are not finite (NaN).  Scores, sums
  * and the softmax are fp32; the codes are multiplied exactly; a weight is kept to 11 bits
  * (fp32 outputs: 22) and to 2^-30 of its row's largest.  What the cache holds outside
  * the positions that a request's queries see is not used.  n_req == 0 or n_q == 0 is

@@ -131,12 +131,14 @@ struct Req {
     int32_t q0, m, len;  // first query, queries, tokens
 };
 
+constexpr int32_t kMostTokens = 0x7fffffff - 64;  // rows past a request's last count on by up to 16
+
 __device__ __forceinline__ Req req_of(const KvqAttendArgs &a, int r)
 {
     Req q;
     q.q0 = a.cu ? clamp_to(a.cu[r], a.n_q) : r;
     q.m = a.cu ? clamp_to(a.cu[r + 1], a.n_q) - q.q0 : 1;
-    q.len = clamp_to(a.lens[r], a.max_len);
+    q.len = clamp_to(a.lens[r], kMostTokens);
     return q;
 }
 
@@ -147,7 +149,7 @@ __device__ __forceinline__ bool few(const KvqAttendArgs &a, int32_t m)
 }
 
 // Positions that rows with limits in [first_limit, last_limit] see: a row with
-// limit L (its position + 1) sees [L - window, L).  Cut from `from` on.
+// limit L (its position + 1) sees [L - window, L), up to max_len.  Cut from `from` on.
 struct Span {
     int32_t first, end, from, splits;
 };
@@ -156,7 +158,7 @@ __device__ __forceinline__ Span span_of(const KvqAttendArgs &a, int32_t first_li
 {
     Span s;
     s.first = a.window > 0 && first_limit > a.window ? first_limit - a.window : 0;
-    s.end = last_limit < 0 ? 0 : last_limit;
+    s.end = clamp_to(last_limit, a.max_len);
     s.from = s.first & ~63;
     s.splits = s.end > s.from ? (s.end - s.from + chunk - 1) / chunk : 0;
     return s;

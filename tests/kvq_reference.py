@@ -131,14 +131,14 @@ def filled(lens, P, H, d, fmt, seed, spread=1.0):
     return c, table
 
 
-def attention(c, q, table, lens, cu, scale, window):
+def attention(c, q, table, lens, cu, scale, window, most=2 ** 31):
     """o, lse, sum p |v|, the largest scale sum |q k| and (tokens x largest value) of every row, in 64 bits.
     q [nq][Hq][d]."""
     nq, Hq, d = q.shape
     G = Hq // c.H
     o, lse = torch.zeros(nq, Hq, d, dtype=torch.float64), torch.full((nq, Hq), -math.inf, dtype=torch.float64)
     mag, size = torch.zeros(nq, Hq, d, dtype=torch.float64), torch.zeros(nq, Hq, dtype=torch.float64)
-    most = torch.zeros(nq, Hq, dtype=torch.float64)
+    top = torch.zeros(nq, Hq, dtype=torch.float64)
     for r, n in enumerate(lens):
         m = cu[r + 1] - cu[r]
         if m <= 0 or n <= 0:
@@ -146,6 +146,7 @@ def attention(c, q, table, lens, cu, scale, window):
         pos = np.arange(n)
         there = np.array([x // c.P < table.shape[1] and 0 <= table[r, x // c.P] < c.pages for x in range(0, n, 16)])
         pos = torch.from_numpy(pos[np.repeat(there, 16)[:n]])
+        pos = pos[pos < most]
         if not len(pos):
             continue
         pg, pl = torch.from_numpy(table[r].astype(np.int64))[pos // c.P], pos % c.P
@@ -165,8 +166,8 @@ def attention(c, q, table, lens, cu, scale, window):
             mag[cu[r]:cu[r + 1], h] = p @ V[:, h // G].abs()
             lse[cu[r]:cu[r + 1], h] = l
             size[cu[r]:cu[r + 1], h] = torch.where(seen, abs(scale) * (qq.abs() @ K[:, h // G].abs().T), 0.0).amax(-1)
-            most[cu[r]:cu[r + 1], h] = (seen * (TOP[c.fmt] * c.scales[pg, h // G, pl // 16, 1].double())).amax(-1) * seen.sum(-1)
-    return o, lse, mag, size, most
+            top[cu[r]:cu[r + 1], h] = (seen * (TOP[c.fmt] * c.scales[pg, h // G, pl // 16, 1].double())).amax(-1) * seen.sum(-1)
+    return o, lse, mag, size, top
 
 
 def limits(w, dtype):
@@ -177,8 +178,8 @@ def limits(w, dtype):
     its 11 bits: numbers under 2^-14 are multiples of 2^-24, rounded by 2^-25 at most, and p is kept as 32 p
     (times a value scale over at most the largest), so each token may be off by 2^-25 / 32 = 2^-30 of the
     largest value (the sum they are divided by is 1 at least, the largest p itself)."""
-    o, lse, mag, size, most = w
+    o, lse, mag, size, top = w
     near = 2.0 ** -20 * (1 + size) + 2.0 ** -14
     half = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}[dtype]
     p = {"bf16": 2.0 ** -11, "f32": 2.0 ** -21}[dtype]
-    return (near + p)[..., None] * mag + half * o.abs() + 2.0 ** -30 * most[..., None], near + 2.0 ** -22 * torch.where(lse.isinf(), 0.0, lse.abs())
+    return (near + p)[..., None] * mag + half * o.abs() + 2.0 ** -30 * top[..., None], near + 2.0 ** -22 * torch.where(lse.isinf(), 0.0, lse.abs())

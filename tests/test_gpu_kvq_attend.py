@@ -50,7 +50,7 @@ def check(sq, c, q, table, lens, new=None, scale=None, window=0, most=None, pad=
     o, lse = run(sq, c, q, table, lens, new, scale, window, most, pad)
     cu = list(range(len(lens) + 1)) if new is None else [0] + np.cumsum(new).tolist()
     sc = q.shape[2] ** -0.5 if scale is None else scale
-    w = ref.attention(c, q, table, lens, cu, sc, window)
+    w = ref.attention(c, q, table, lens, cu, sc, window, 2 ** 31 if most is None else most)
     lo, ll = ref.limits(w, "bf16" if q.dtype == torch.bfloat16 else "f32")
     assert torch.isfinite(o).all()
     off = (o - w[0]).abs()
@@ -100,9 +100,7 @@ def test_token_long(sq, fmt, P):
     q = queries(3, 4, 3, 128, "bf16")
     check(sq, c, q, t, lens)
     check(sq, c, q, t, lens, most=60000)
-    o, lse = run(sq, c, q, t, lens, most=5000)
-    w = ref.attention(c, q, t, [5000, 3, 0, 5000], list(range(5)), 128 ** -0.5, 0)
-    assert ((o - w[0]).abs() <= ref.limits(w, "bf16")[0]).all()
+    check(sq, c, q, t, lens, most=5000)
 
 
 def test_token_of_many_requests(sq):
@@ -163,6 +161,19 @@ def test_capacity_larger_than_the_queries(sq, new):
     lens = [1000]
     c, t = ref.filled(lens, 64, 2, 64, "int8", 5)
     check(sq, c, queries(4, sum(new), 4, 64, "bf16"), t, lens, new=new, pad=500 - sum(new))
+
+
+@pytest.mark.parametrize("window", [0, 90])
+def test_requests_longer_than_the_bound(sq, window):
+    """Positions from max_len on, or past the table, are not seen; queries keep their places."""
+    new, ctx = [300, 1, 40], [100, 399, 500]
+    lens = [a + b for a, b in zip(ctx, new)]
+    c, t = ref.filled(lens, 32, 2, 64, "int8", 15)
+    q = queries(4, sum(new), 4, 64, "bf16")
+    for most in (0, 1, 33, 250, 399, 512):
+        check(sq, c, q, t, lens, new=new, window=window, most=most)
+    t = np.ascontiguousarray(t[:, :10])
+    check(sq, c, q, t, lens, new=new, window=window)  # the reference knows rows that end
 
 
 def test_more_queries_than_tokens(sq):
