@@ -53,15 +53,13 @@ struct KvqAttendArgs {
     int32_t few_on;              // 0: every request goes to the tile form
     int32_t q_tiles, rows;       // 16-row tiles and rows of partial results per (request, head)
     int32_t chunk, splits;       // tokens per split, splits of the longest request
-    // many queries: tiles of kTileRows rows
+    // many queries: tiles of 256 or 128 rows
     int32_t tiles;               // tile slots over all requests, 0: none can need them
     int32_t t_chunk, t_splits;
 };
 
-constexpr int kTileRows = 128;
-
 // Fills the split fields from the sizes; returns the bytes of partial results.
-uint64_t kvq_plan(KvqAttendArgs &a);
+uint64_t kvq_plan(KvqAttendArgs &a, bool bf16);
 // Upper bound of those bytes over every call with at most these sizes.
 uint64_t kvq_plan_bound(int32_t n, int32_t n_q, int32_t kv_heads, int32_t q_heads, int32_t d, int32_t max_len);
 hipError_t launch_kvq_attend(const KvqAttendArgs &a, bool bf16, hipStream_t st);

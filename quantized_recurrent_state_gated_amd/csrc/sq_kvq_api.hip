@@ -146,7 +146,7 @@ int sq_kvq_attention(const sq_kvq_cache *cache, const void *q, int64_t q_stride,
     a.sign = scale > 0.0f ? 1.0f : scale < 0.0f ? -1.0f : 0.0f;
     a.o = o;
     a.lse = lse;
-    const uint64_t need = kvq_plan(a);
+    const uint64_t need = kvq_plan(a, dtype == SQ_BF16);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return SQ_ERR_INVALID;
     a.part = static_cast<float *>(workspace);
     return status(launch_kvq_attend(a, dtype == SQ_BF16, (hipStream_t)stream));
