@@ -1,6 +1,6 @@
 // sq_kvq.h -- internal interface between the host code (sq_kvq_api.hip) and the
 // kernels of the 8-bit paged key-value cache (sq_kvq.hip: write and read back,
-// sq_kvq_attend.hip: attention).  Not installed, not part of the ABI.
+// sq_kvq_few.hip, sq_kvq_tiles.hip: attention).  Not installed, not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -54,14 +54,19 @@ struct KvqAttendArgs {
     int32_t q_tiles, rows;       // 16-row tiles and rows of partial results per (request, head)
     int32_t chunk, splits;       // tokens per split, splits of the longest request
     // many queries: tiles of 256 or 128 rows
+    int32_t tile_rows;
     int32_t tiles;               // tile slots over all requests, 0: none can need them
     int32_t t_chunk, t_splits;
 };
+
+// Whether tiles may have 256 rows: two waves on every SIMD, where the registers allow it.
+constexpr bool tiles_of_256(bool bf16, int d) { return d <= 96 || (bf16 && d <= 128); }
 
 // Fills the split fields from the sizes; returns the bytes of partial results.
 uint64_t kvq_plan(KvqAttendArgs &a, bool bf16);
 // Upper bound of those bytes over every call with at most these sizes.
 uint64_t kvq_plan_bound(int32_t n, int32_t n_q, int32_t kv_heads, int32_t q_heads, int32_t d, int32_t max_len);
+hipError_t launch_kvq_tiles(const KvqAttendArgs &a, bool bf16, hipStream_t st);
 hipError_t launch_kvq_attend(const KvqAttendArgs &a, bool bf16, hipStream_t st);
 
 }  // namespace sqk

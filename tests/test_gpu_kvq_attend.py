@@ -335,3 +335,16 @@ def test_workspaces_of_smaller_calls(sq):
         big = sq.sq_kvq_attention_workspace(dev, n, nq, 12, most)
         n2, q2, m2 = int(rng.integers(1, n + 1)), int(rng.integers(1, nq + 1)), int(rng.integers(0, most + 1))
         assert sq.sq_kvq_attention_workspace(dev, n2, q2, 12, m2) <= big
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtype,d,window", [("bf16", 128, 0), ("bf16", 64, 200), ("bf16", 96, 0), ("f32", 64, 0),
+                                            ("f32", 96, 100), ("f32", 32, 0), ("bf16", 32, 0), ("f32", 128, 0)])
+def test_prompts_that_fill_the_card(sq, fmt, dtype, d, window):
+    """Enough rows for the larger tiles, unsplit; a request of few queries and one of none among them, and
+    pages that do not exist."""
+    new, ctx = [700, 2, 0, 331], [37, 100, 5, 0]
+    lens = [a + b for a, b in zip(ctx, new)]
+    c, t = ref.filled(lens, 16, 8, d, fmt, d)
+    t[0, 20:23] = -1
+    check(sq, c, queries(d, sum(new), 64, d, dtype), t, lens, new=new, window=window, pad=5)
