@@ -50,15 +50,40 @@ __global__ __launch_bounds__(2 * ROWS, tiles_of_256(sizeof(T) == 2, D) ? 2 : 1) 
     const int part = WAVES == 8 ? (wv & 3) * 2 + grp : wv;          // which 32 rows: few rows spread over both halves
     const unsigned heads = (unsigned)a.c.heads, tiles = (unsigned)a.tiles;
     const int h = (int)(blockIdx.x % heads);
-    const int64_t slot = tiles - 1 - blockIdx.x / heads % tiles;  // late tiles see the most: first
+    const int slot = (int)(blockIdx.x / heads % tiles);
     const int sp = (int)(blockIdx.x / heads / tiles);
 
-    const int r = wave_count(a.n, [&](int i) { return (int64_t)clamp_to(a.cu[i], a.n_q) * a.group / ROWS + i <= slot; }) - 1;
-    if (r < 0) return;
+    // The slot's request and tile: longest requests first, so that short ones fill in
+    // behind them (up to 64 requests; more go in their order), and of a request the late
+    // tiles, which see the most.  (Six ragged
+    // pieces of 1,024 tokens at most behind up to 6,000: 345 us as they come, 310 so.)
+    int r;
+    int64_t tile;
+    if (a.n <= 64) {
+        int32_t len = -1, count = 0;
+        if (lane < a.n) {
+            const Req q = req_of(a, lane);
+            len = q.len;
+            count = q.m < 1 || few(a, q.m) ? 0 : (int32_t)(((int64_t)q.m * a.group + ROWS - 1) / ROWS);
+        }
+        int32_t first = 0;
+        for (int i = 0; i < a.n; i++) {
+            const int32_t l = __builtin_amdgcn_readlane(len, i), k = __builtin_amdgcn_readlane(count, i);
+            if (l > len || (l == len && i < lane)) first += k;
+        }
+        const uint64_t mine = __ballot(slot >= first && slot - first < count);
+        if (!mine) return;
+        r = __builtin_ctzll(mine);
+        tile = __builtin_amdgcn_readlane(count, r) - 1 - (slot - __builtin_amdgcn_readlane(first, r));
+    } else {
+        const int back = (int)tiles - 1 - slot;
+        r = wave_count(a.n, [&](int i) { return (int64_t)clamp_to(a.cu[i], a.n_q) * a.group / ROWS + i <= back; }) - 1;
+        if (r < 0) return;
+        tile = back - ((int64_t)clamp_to(a.cu[r], a.n_q) * a.group / ROWS + r);
+    }
     const Req q = req_of(a, r);
     if (q.m < 1 || few(a, q.m)) return;
-    const int64_t rows = (int64_t)q.m * a.group;
-    const int64_t row0 = (slot - ((int64_t)q.q0 * a.group / ROWS + r)) * ROWS;
+    const int64_t rows = (int64_t)q.m * a.group, row0 = tile * ROWS;
     if (row0 >= rows) return;
     const bool active = row0 + part * 32 < rows;  // the wave has rows (it stages tokens in any case)
     const int64_t row = row0 + part * 32 + c;
@@ -212,6 +237,14 @@ __global__ __launch_bounds__(2 * ROWS, tiles_of_256(sizeof(T) == 2, D) ? 2 : 1) 
 #pragma unroll
                 for (int k2 = 0; k2 < PARTS; k2++) x[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, qf[i][k2], x[u], 0, 0, 0);
             }
+        // four operands ahead of the products
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * NS - 4; i++) {
+            __builtin_amdgcn_sched_group_barrier(0x8, PARTS, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x8, PARTS * 4, 0);
     };
     auto outputs = [&](int buf) {
         const _Float16 *vp = sm_v[buf] + c * VP + 8 * hh;
@@ -223,6 +256,13 @@ __global__ __launch_bounds__(2 * ROWS, tiles_of_256(sizeof(T) == 2, D) ? 2 : 1) 
 #pragma unroll
                 for (int k2 = 0; k2 < PARTS; k2++) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[b][k2], acc[i], 0, 0, 0);
             }
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int i = 0; i < 4 * ND - 4; i++) {
+            __builtin_amdgcn_sched_group_barrier(0x8, PARTS, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x8, PARTS * 4, 0);
     };
     // p and the sum of it from x, by the maximum so far
     auto weigh = [&](const f32x4 (&sc)[4], const float (&fk)[4]) {
