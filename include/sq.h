@@ -411,6 +411,8 @@ int sq_paged_attention(const sq_kv_cache *cache, const void *q, int64_t q_stride
  *     SQ_KVQ_INT8  c = u - 128, an integer in [-127, 127] (excess form, as the
  *                  8-bit codes of the pool)
  *     SQ_KVQ_E4M3  c = the OCP e4m3 number u (no infinities, largest 448)
+ * Scales written by sq_kvq_append are at least 2^-100; in a cache made elsewhere they
+ * may be smaller, or zero, and attention may take value scales below that as 2^-100.
  * Requests, pages and block tables are those of the paged cache above
  * (sq_block_tables).  Pages may hold anything past a request's last token,
  * scales included. */

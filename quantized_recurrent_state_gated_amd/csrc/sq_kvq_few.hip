@@ -453,7 +453,8 @@ constexpr int64_t kTileWgs = 256, kMinTileChunk = 1024;
 
 uint64_t part_bytes(int64_t rows, int32_t d) { return (uint64_t)rows * (uint64_t)(d + 2) * 4; }
 
-int64_t rows_few(bool one, int64_t group) { return one || group > 16 ? group : 16; }
+// rows of a (request, head), in fours where the tile form's partial results come behind them
+int64_t rows_few(bool one, int64_t group) { return one ? group : group > 16 ? (group + 3) / 4 * 4 : 16; }
 
 }  // namespace
 

@@ -206,9 +206,11 @@ __global__ __launch_bounds__(2 * ROWS, tiles_of_256(sizeof(T) == 2, D) ? 2 : 1) 
     };
     auto stage_scales = [&](int ring, f32x2 sc) {
         if (!scaler) return;
+        // weights are made with their value scale in the exponent: it has a logarithm
+        const float v = fmaxf(sc[1], 0x1p-100f);
         float *to = reinterpret_cast<float *>(sm_s[ring]) + lane;
-        to[0] = sc[0], to[4] = sc[1];
-        if constexpr (PARTS == 1) to[8] = __builtin_amdgcn_logf(sc[1]), to[12] = sc[1] > 0.0f ? 1.0f / sc[1] : 0.0f;
+        to[0] = sc[0], to[4] = v;
+        if constexpr (PARTS == 1) to[8] = __builtin_amdgcn_logf(v), to[12] = 1.0f / v;
     };
 
     f32x16 acc[ND], x[2];

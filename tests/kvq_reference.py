@@ -177,9 +177,10 @@ def limits(w, dtype):
     is rounded once.  Far below the largest probability of a row, p has the last place of float16 and not
     its 11 bits: numbers under 2^-14 are multiples of 2^-24, rounded by 2^-25 at most, and p is kept as 32 p
     (times a value scale over at most the largest), so each token may be off by 2^-25 / 32 = 2^-30 of the
-    largest value (the sum they are divided by is 1 at least, the largest p itself)."""
+    largest value (the sum they are divided by is 1 at least, the largest p itself).  A value scale below 2^-100
+    may count as that: codes are 448 at most."""
     o, lse, mag, size, top = w
     near = 2.0 ** -20 * (1 + size) + 2.0 ** -14
     half = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}[dtype]
     p = {"bf16": 2.0 ** -11, "f32": 2.0 ** -21}[dtype]
-    return (near + p)[..., None] * mag + half * o.abs() + 2.0 ** -30 * top[..., None], near + 2.0 ** -22 * torch.where(lse.isinf(), 0.0, lse.abs())
+    return (near + p)[..., None] * mag + half * o.abs() + 2.0 ** -30 * top[..., None] + 448 * 2.0 ** -100, near + 2.0 ** -22 * torch.where(lse.isinf(), 0.0, lse.abs())

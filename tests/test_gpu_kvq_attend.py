@@ -348,3 +348,20 @@ def test_prompts_that_fill_the_card(sq, fmt, dtype, d, window):
     c, t = ref.filled(lens, 16, 8, d, fmt, d)
     t[0, 20:23] = -1
     check(sq, c, queries(d, sum(new), 64, d, dtype), t, lens, new=new, window=window, pad=5)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("new,ctx", BOTH)
+def test_scales_of_zero(sq, fmt, new, ctx):
+    """A cache made elsewhere may hold blocks of zeros with a scale of zero: their values are zero and their
+    tokens count, their keys' scores are zero.  All values of one request are."""
+    lens = [a + b for a, b in zip(ctx, new)]
+    c, t = ref.filled(lens, 16, 2, 64, fmt, 13)
+    for r, n in enumerate(lens):
+        for i, x in enumerate(range(0, n, 16)):
+            if i % 3 == 1 or r == 1:
+                c.scales[t[r, x // 16], :, :, 1] = 0.0
+            if i % 4 == 2:
+                c.scales[t[r, x // 16], :, :, 0] = 0.0
+    for dtype in ("bf16", "f32"):
+        check(sq, c, queries(6, sum(new), 4, 64, dtype), t, lens, new=new)
