@@ -301,6 +301,8 @@ __global__ __launch_bounds__(256) void k_kvq_few(KvqAttendArgs a)
 
 // ---------------------------------------------------------------- join of splits
 
+constexpr int kWaveSplits = 8;  // up to so many splits of a tile a wave joins a row
+
 // A workgroup joins one row: its four waves take every fourth split, four in flight.
 template <typename T, int D>
 __device__ __forceinline__ void join_row(const KvqAttendArgs &a, const float *src, const float *ml, int splits, int64_t out)
@@ -355,6 +357,38 @@ __device__ __forceinline__ void join_row(const KvqAttendArgs &a, const float *sr
     if (a.lse && threadIdx.x == 0) a.lse[out] = log_sum(M, L);
 }
 
+// The same by one wave, for few splits.
+template <typename T, int D>
+__device__ __forceinline__ void join_row_wave(const KvqAttendArgs &a, const float *src, const float *ml, int splits, int64_t out)
+{
+    constexpr int PER = (D + 63) / 64;
+    const int lane = threadIdx.x & 63;
+    float M = -kInf;
+    for (int i = 0; i < splits; i++) M = fmaxf(M, ml[2 * i]);
+    float o[PER], L = 0.0f;
+#pragma unroll
+    for (int j = 0; j < PER; j++) o[j] = 0.0f;
+    for (int i = 0; i < splits; i++) {
+        const float m = ml[2 * i], f = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(m - M);
+        L = fmaf(ml[2 * i + 1], f, L);
+#pragma unroll
+        for (int j = 0; j < PER; j++) {
+            const int d = j * 64 + lane;
+            if (D % 64 == 0 || d < D) o[j] = fmaf(src[(int64_t)i * D + d], f, o[j]);
+        }
+    }
+    const float inv = inverse_sum(M, L);
+    T *dst = reinterpret_cast<T *>(a.o) + out * D;
+#pragma unroll
+    for (int j = 0; j < PER; j++) {
+        const int d = j * 64 + lane;
+        if (D % 64 != 0 && d >= D) continue;
+        if constexpr (sizeof(T) == 4) dst[d] = o[j] * inv;
+        else dst[d] = __builtin_bit_cast(uint16_t, (__bf16)(o[j] * inv));
+    }
+    if (a.lse && lane == 0) a.lse[out] = log_sum(M, L);
+}
+
 // row `id` of the few-query form's partial results
 template <typename T, int D>
 __device__ __forceinline__ void join_few(const KvqAttendArgs &a, unsigned id)
@@ -392,15 +426,24 @@ __device__ __forceinline__ void join_tiles(const KvqAttendArgs &a, int64_t out)
     if (s.splits <= 1) return;  // written already
     const float *part = a.part + (int64_t)a.n * a.c.heads * a.rows * (a.splits > 1 ? a.splits : 0) * (D + 2);
     const int64_t at = out * a.t_splits;
-    join_row<T, D>(a, part + at * D, part + (int64_t)a.n_q * a.q_heads * a.t_splits * D + at * 2, s.splits, out);
+    const float *ml = part + (int64_t)a.n_q * a.q_heads * a.t_splits * D + at * 2;
+    if (a.t_splits <= kWaveSplits) join_row_wave<T, D>(a, part + at * D, ml, s.splits, out);
+    else join_row<T, D>(a, part + at * D, ml, s.splits, out);
 }
 
-// Both forms' rows in one launch, those of the tiles first.
+// Both forms' rows in one launch, those of the tiles first: a workgroup each, or a wave
+// each where there are few splits.
 template <typename T, int D>
-__global__ __launch_bounds__(256) void k_kvq_join(KvqAttendArgs a, unsigned tile_rows)
+__global__ __launch_bounds__(256) void k_kvq_join(KvqAttendArgs a, unsigned tile_wgs)
 {
-    if (blockIdx.x < tile_rows) join_tiles<T, D>(a, blockIdx.x);
-    else join_few<T, D>(a, blockIdx.x - tile_rows);
+    if (blockIdx.x >= tile_wgs) {
+        join_few<T, D>(a, blockIdx.x - tile_wgs);
+    } else if (a.t_splits <= kWaveSplits) {
+        const int64_t out = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+        if (out < (int64_t)a.n_q * a.q_heads) join_tiles<T, D>(a, out);
+    } else {
+        join_tiles<T, D>(a, blockIdx.x);
+    }
 }
 
 // ---------------------------------------------------------------- launches
@@ -410,8 +453,9 @@ hipError_t attend_tfd(const KvqAttendArgs &a, hipStream_t st)
 {
     const int64_t units = (int64_t)a.n * a.c.heads;
     const int64_t few_grid = units * a.q_tiles * a.splits, tile_grid = (int64_t)a.tiles * a.c.heads * a.t_splits;
-    const int64_t few_rows = a.splits > 1 ? units * a.rows : 0, tile_rows = a.t_splits > 1 ? (int64_t)a.n_q * a.q_heads : 0;
-    if (!grid_fits(few_grid, 256) || !grid_fits(tile_grid, 2 * a.tile_rows) || !grid_fits(few_rows + tile_rows, 256))
+    const int64_t few_rows = a.splits > 1 ? units * a.rows : 0, rows = a.t_splits > 1 ? (int64_t)a.n_q * a.q_heads : 0;
+    const int64_t tile_wgs = a.t_splits <= kWaveSplits ? (rows + 3) / 4 : rows;
+    if (!grid_fits(few_grid, 256) || !grid_fits(tile_grid, 2 * a.tile_rows) || !grid_fits(few_rows + tile_wgs, 256))
         return hipErrorInvalidConfiguration;
     if (a.tiles > 0)
         if (hipError_t e = launch_kvq_tiles(a, sizeof(T) == 2, st)) return e;
@@ -419,8 +463,8 @@ hipError_t attend_tfd(const KvqAttendArgs &a, hipStream_t st)
         hipLaunchKernelGGL((k_kvq_few<T, E4M3, D>), dim3((unsigned)few_grid), dim3(256), 0, st, a);
         if (hipError_t e = hipGetLastError()) return e;
     }
-    if (few_rows + tile_rows > 0)
-        hipLaunchKernelGGL((k_kvq_join<T, D>), dim3((unsigned)(few_rows + tile_rows)), dim3(256), 0, st, a, (unsigned)tile_rows);
+    if (few_rows + tile_wgs > 0)
+        hipLaunchKernelGGL((k_kvq_join<T, D>), dim3((unsigned)(few_rows + tile_wgs)), dim3(256), 0, st, a, (unsigned)tile_wgs);
     return hipGetLastError();
 }
 
@@ -467,9 +511,11 @@ uint64_t kvq_plan(KvqAttendArgs &a, bool bf16)
     auto span = [&](int64_t apart) { return most == a.max_len || most + apart + 63 > a.max_len ? (int64_t)a.max_len : most + apart + 63; };
     uint64_t bytes = 0;
 
-    // one request that may have many queries is left to the tile form, which takes
-    // any number; of several, each goes to the form of its own size
-    a.few_on = !tiled || a.n > 1;
+    // The tile form takes any number of queries.  The other one is worth its launches where
+    // requests of few queries are likely (the mean says so) or have long contexts: a
+    // single token among prompts, over 500, 1,000 and 2,000 tokens (31 beside a prompt of
+    // 512, 8 heads of 4): 50, 72 and 111 us with it, 43, 67 and 114 without.
+    a.few_on = !tiled || (a.n > 1 && (most > 2048 || (int64_t)a.n_q * a.group <= 16 * (int64_t)a.n));
     a.rows = (int32_t)rows_few(one, a.group);
     a.q_tiles = a.few_on ? (a.rows + 15) / 16 : 0;
     a.chunk = 256;
@@ -496,11 +542,21 @@ uint64_t kvq_plan(KvqAttendArgs &a, bool bf16)
         auto cut = [&](int32_t rows) {
             a.tile_rows = rows;
             a.tiles = (int32_t)((int64_t)a.n_q * a.group / rows + a.n);
-            const int64_t wgs = (int64_t)a.tiles * heads, n = wgs > kTileWgs / 2 ? 1 : kTileWgs / wgs;
+            // what is likely of them: every request may end in a part of a tile, or have none
+            int64_t wgs = ((int64_t)a.n_q * a.group / rows + a.n / 4) * heads;
+            if (wgs < heads) wgs = heads;
+            const int64_t n = wgs > kTileWgs / 2 ? 1 : kTileWgs / wgs;
             int64_t c = ((span(rows - 1) + n - 1) / n + 63) / 64 * 64;
             if (c < kMinTileChunk) c = kMinTileChunk;
-            const int64_t s = (span(rows - 1) + c - 1) / c;
-            a.t_chunk = (int32_t)c;
+            int64_t s = (span(rows - 1) + c - 1) / c;
+            // a split saves turns (of 64 tokens, 2.2 us) and costs a launch, and partial
+            // results written and read: 26,000 rows x 2 splits some 25 us
+            const int64_t out = (int64_t)a.n_q * a.q_heads, turns = span(rows - 1) / 64;
+            if (s > 1 && turns - turns / s <= 4 + out / 2500 + out * s * a.c.d / 1100000) {
+                s = 1;
+                c = (span(rows - 1) + 63) / 64 * 64;
+            }
+            a.t_chunk = (int32_t)(c < 64 ? 64 : c);
             a.t_splits = (int32_t)(s < 1 ? 1 : s);
         };
         // 256 rows where such tiles, or their splits, fill the card; few short ones end
@@ -525,9 +581,10 @@ uint64_t kvq_plan_bound(int32_t n, int32_t n_q, int32_t kv_heads, int32_t q_head
     const int64_t fine = (len + kMinChunk - 1) / kMinChunk, coarse = (len + kMaxChunk - 1) / kMaxChunk;
     const int64_t cut = 24 * kMost + R > R * coarse ? 24 * kMost + R : R * coarse;
     const int64_t few = R * fine < cut ? R * fine : cut;
-    // Tiles: split only where they are at most kTileWgs / 2, into kTileWgs / tiles
+    // Tiles of 256 rows: rows <= 512 x the tiles they are taken for, which are split only
+    // if they are at most kTileWgs / 2, into kTileWgs over their number
     const int64_t whole = (int64_t)n_q * q_heads * ((len + kMinTileChunk - 1) / kMinTileChunk);
-    const int64_t tiled = whole < kTileWgs * 256 ? whole : kTileWgs * 256;
+    const int64_t tiled = whole < kTileWgs * 512 ? whole : kTileWgs * 512;
     return part_bytes(few, d) + part_bytes(tiled, d);
 }
 
