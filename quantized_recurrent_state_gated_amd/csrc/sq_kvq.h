@@ -59,8 +59,10 @@ struct KvqAttendArgs {
     int32_t t_chunk, t_splits;
 };
 
-// Whether tiles may have 256 rows: two waves on every SIMD, where the registers allow it.
-constexpr bool tiles_of_256(bool bf16, int d) { return d <= 96 || (bf16 && d <= 128); }
+// Whether the tile kernel's registers leave room for two waves on a SIMD.
+constexpr bool two_a_simd(bool bf16, int d) { return d <= 96 || (bf16 && d <= 128); }
+// Whether tiles of 256 rows pay anywhere (kvq_plan says where).
+constexpr bool tiles_of_256(bool bf16, int d) { return bf16 && d == 128; }
 
 // Fills the split fields from the sizes; returns the bytes of partial results.
 uint64_t kvq_plan(KvqAttendArgs &a, bool bf16);

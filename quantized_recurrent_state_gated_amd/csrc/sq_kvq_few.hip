@@ -493,7 +493,7 @@ hipError_t attend_t(const KvqAttendArgs &a, hipStream_t st)
 constexpr int64_t kMost = 4096, kFew = 512, kLongSplit = 2048, kMinChunk = 256;
 
 // Many queries: splits only where the tiles alone leave the card idle.
-constexpr int64_t kTileWgs = 256, kMinTileChunk = 1024;
+constexpr int64_t kCus = 256, kMinTileChunk = 1024;
 
 uint64_t part_bytes(int64_t rows, int32_t d) { return (uint64_t)rows * (uint64_t)(d + 2) * 4; }
 
@@ -543,9 +543,10 @@ uint64_t kvq_plan(KvqAttendArgs &a, bool bf16)
             a.tile_rows = rows;
             a.tiles = (int32_t)((int64_t)a.n_q * a.group / rows + a.n);
             // what is likely of them: every request may end in a part of a tile, or have none
-            int64_t wgs = ((int64_t)a.n_q * a.group / rows + a.n / 4) * heads;
-            if (wgs < heads) wgs = heads;
-            const int64_t n = wgs > kTileWgs / 2 ? 1 : kTileWgs / wgs;
+            const int64_t all = (int64_t)a.n_q * a.group, likely = a.n == 1 ? (all + rows - 1) / rows : all / rows + a.n / 4;
+            const int64_t wgs = (likely < 1 ? 1 : likely) * heads;
+            const int64_t at_once = rows == 128 && two_a_simd(bf16, a.c.d) ? 2 * kCus : kCus;
+            const int64_t n = wgs > at_once / 2 ? 1 : at_once / wgs;
             int64_t c = ((span(rows - 1) + n - 1) / n + 63) / 64 * 64;
             if (c < kMinTileChunk) c = kMinTileChunk;
             int64_t s = (span(rows - 1) + c - 1) / c;
@@ -559,12 +560,22 @@ uint64_t kvq_plan(KvqAttendArgs &a, bool bf16)
             a.t_chunk = (int32_t)(c < 64 ? 64 : c);
             a.t_splits = (int32_t)(s < 1 ? 1 : s);
         };
-        // 256 rows where such tiles, or their splits, fill the card; few short ones end
-        // sooner as 128 rows, whose waves all multiply and weigh at once (three windowed
-        // prompts of 700 tokens, 36 tiles of 256: 33 us against 20; 33 tokens behind
-        // 60,000, split: 69 against 82; one of 8,192 tokens: 600 against 640)
-        if (tiles_of_256(bf16, a.c.d)) cut(256);
-        if (a.tile_rows == 128 || (a.t_splits == 1 && (int64_t)a.tiles * heads < kTileWgs)) cut(128);
+        // Tiles of 256 rows stage a token half as often, and their waves take turns; of 128
+        // rows there are two workgroups a unit, each of which ends beside the other's work.
+        // Measured (8 heads of 4, us with 256 and 128):
+        //   long contexts, many rounds of tiles: one prompt of 8,192 572 and 600
+        //   fewer rounds, the last one decides: one of 6,000 344 and 336, 8 x 512 behind 4,000
+        //   315 and 333, two sets of 6 ragged behind 6,000 274 and 260, 274 and 275
+        //   short ones: 20 x 800 236 and 212, 8,192 tokens in a window of 1,024 196 and 185
+        //   few rows, 256 hold them as well as 2 x 128: 33 behind 60,000 76 and 86, 30 x 40
+        //   behind 8,000 256 and 292; not so: 20 behind 60,000 69 and 52, 80 behind 30,000
+        //   82 and 72
+        // and where d is not 128, or two float16 stand for a query, 128 everywhere (d = 64, one
+        // prompt of 8,192: 502 and 399, 20 x 800 195 and 151).
+        const int64_t mean = ((int64_t)a.n_q * a.group + a.n - 1) / a.n;
+        const bool even = (mean + 255) / 256 * 256 <= (mean + 127) / 128 * 128;
+        if (tiles_of_256(bf16, a.c.d) && most >= 4096 && even) cut(256);
+        if (a.tile_rows == 128 || (mean > 256 && (int64_t)a.tiles * heads < 3 * kCus)) cut(128);
         if (a.t_splits > 1) bytes += part_bytes((int64_t)a.n_q * a.q_heads * a.t_splits, a.c.d);
     }
     return bytes;
@@ -582,9 +593,10 @@ uint64_t kvq_plan_bound(int32_t n, int32_t n_q, int32_t kv_heads, int32_t q_head
     const int64_t cut = 24 * kMost + R > R * coarse ? 24 * kMost + R : R * coarse;
     const int64_t few = R * fine < cut ? R * fine : cut;
     // Tiles of 256 rows: rows <= 512 x the tiles they are taken for, which are split only
-    // if they are at most kTileWgs / 2, into kTileWgs over their number
+    // if their workgroups are at most kCus / 2, into kCus over their number; or of 128
+    // rows, and twice as many workgroups
     const int64_t whole = (int64_t)n_q * q_heads * ((len + kMinTileChunk - 1) / kMinTileChunk);
-    const int64_t tiled = whole < kTileWgs * 512 ? whole : kTileWgs * 512;
+    const int64_t tiled = whole < kCus * 512 ? whole : kCus * 512;
     return part_bytes(few, d) + part_bytes(tiled, d);
 }
 

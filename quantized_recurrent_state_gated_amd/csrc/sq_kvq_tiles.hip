@@ -28,13 +28,13 @@ using namespace kvq;
 // cycles from the other wave's vector instructions on the SIMD (measured), so turns of
 // products beside turns of weights cannot do with less than about 1,800 cycles
 // for two waves' halves; they take 2,400.  One causal prompt of 8,192 tokens, 32 query and 8
-// key-value heads, d = 128 in integer codes: 583 to 610 us, 900 to 945 TFLOP/s (a
+// key-value heads, d = 128 in integer codes: 572 to 587 us, 935 to 960 TFLOP/s (a
 // float16 library product of 8192^3 reaches 1,092).  On the way: 1,046 us with one wave a
 // SIMD, 660 with two that are not kept apart, 820 with turns but page ids waited for one by
 // one, 631 with the maximum looked for in every tile.
 
 template <typename T, bool E4M3, int D, int ROWS>
-__global__ __launch_bounds__(2 * ROWS, tiles_of_256(sizeof(T) == 2, D) ? 2 : 1) void k_kvq_tiles(KvqAttendArgs a)
+__global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) void k_kvq_tiles(KvqAttendArgs a)
 {
     constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
     constexpr int WAVES = ROWS / 32, TPB = 64 * WAVES;
@@ -48,10 +48,13 @@ __global__ __launch_bounds__(2 * ROWS, tiles_of_256(sizeof(T) == 2, D) ? 2 : 1) 
     const int wv = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int grp = WAVES == 8 ? wv >> 2 : 0;                       // which half of the waves: the two take turns
     const int part = WAVES == 8 ? (wv & 3) * 2 + grp : wv;          // which 32 rows: few rows spread over both halves
-    const unsigned heads = (unsigned)a.c.heads, tiles = (unsigned)a.tiles;
+    // A slot's splits lie side by side: slots that no tile takes come last.  (Between the
+    // others they leave half of the card's engines without work, as workgroups go to these
+    // in turn: 64 tokens behind 30,000, one slot of two taken: 96 us, 57 so.)
+    const unsigned heads = (unsigned)a.c.heads, splits = (unsigned)a.t_splits;
     const int h = (int)(blockIdx.x % heads);
-    const int slot = (int)(blockIdx.x / heads % tiles);
-    const int sp = (int)(blockIdx.x / heads / tiles);
+    const int sp = (int)(blockIdx.x / heads % splits);
+    const int slot = (int)(blockIdx.x / heads / splits);
 
     // The slot's request and tile: longest requests first, so that short ones fill in
     // behind them (up to 64 requests; more go in their order), and of a request the late
@@ -76,7 +79,7 @@ __global__ __launch_bounds__(2 * ROWS, tiles_of_256(sizeof(T) == 2, D) ? 2 : 1) 
         r = __builtin_ctzll(mine);
         tile = __builtin_amdgcn_readlane(count, r) - 1 - (slot - __builtin_amdgcn_readlane(first, r));
     } else {
-        const int back = (int)tiles - 1 - slot;
+        const int back = a.tiles - 1 - slot;
         r = wave_count(a.n, [&](int i) { return (int64_t)clamp_to(a.cu[i], a.n_q) * a.group / ROWS + i <= back; }) - 1;
         if (r < 0) return;
         tile = back - ((int64_t)clamp_to(a.cu[r], a.n_q) * a.group / ROWS + r);

@@ -365,3 +365,54 @@ def test_scales_of_zero(sq, fmt, new, ctx):
                 c.scales[t[r, x // 16], :, :, 0] = 0.0
     for dtype in ("bf16", "f32"):
         check(sq, c, queries(6, sum(new), 4, 64, dtype), t, lens, new=new)
+
+
+# ---------------------------------------------------------------- prompts behind long contexts, wide heads
+
+# Tiles hold more rows there: four ragged requests of few rows, and many rows at once.
+LONG = [([40, 0, 64, 56], [60, 5, 0, 2100], 4, 1), ([640, 2, 0, 421], [37, 100, 5, 700], 256, 16)]
+
+
+def long_table(t, P, span=4500):
+    """The table with room for more positions, whose pages do not exist."""
+    return np.concatenate([t, np.full((t.shape[0], -(-span // P)), -1, t.dtype)], 1)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("new,ctx,H,Hkv", LONG)
+@pytest.mark.parametrize("P", [16, 128])
+def test_larger_tiles(sq, fmt, new, ctx, H, Hkv, P):
+    """Ragged requests, one without new tokens, pages that do not exist, value scales far apart."""
+    lens = [a + b for a, b in zip(ctx, new)]
+    c, t = ref.filled(lens, P, Hkv, 128, fmt, 17, spread=8.0)
+    c.scales[..., 0] = torch.where(c.held.view(c.pages, 1, -1, 16).any(-1), 1 / 64, c.scales[..., 0])
+    t = long_table(t, P)
+    q = queries(17, sum(new), H, 128, "bf16")
+    check(sq, c, q, t, lens, new=new, most=4400, pad=2)
+    t[0, 0] = -1
+    t[3, 256 // P:512 // P] = 10 ** 6
+    check(sq, c, q, t, lens, new=new, most=4400, scale=-0.2)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("new,ctx,window", [([40], [6000], 4500), ([33], [9000], 0), ([64], [6900], 4096),
+                                            ([50, 60], [5000, 4100], 4200)])
+def test_larger_tiles_behind_long_contexts(sq, fmt, new, ctx, window):
+    lens = [a + b for a, b in zip(ctx, new)]
+    c, t = ref.filled(lens, 32, 2, 128, fmt, 19)
+    check(sq, c, queries(19, sum(new), 8, 128, "bf16"), t, lens, new=new, window=window)
+
+
+@pytest.mark.parametrize("new,ctx,H,Hkv", LONG)
+def test_larger_tiles_of_queries_that_are_not_finite(sq, new, ctx, H, Hkv):
+    lens = [a + b for a, b in zip(ctx, new)]
+    c, t = ref.filled(lens, 16, Hkv, 128, "int8", 21)
+    t = long_table(t, 16)
+    q = queries(21, sum(new), H, 128, "bf16")
+    o, lse = run(sq, c, q, t, lens, new, most=4400)
+    hit = torch.zeros(sum(new), H, dtype=torch.bool)
+    q[0, 1, 9], q[-1, 3, 0], q[2, 0, 127] = NAN, INF, -INF
+    hit[0, 1] = hit[-1, 3] = hit[2, 0] = True
+    o2, lse2 = run(sq, c, q, t, lens, new, most=4400)
+    assert torch.isnan(o2[hit]).all() and torch.isnan(lse2[hit]).all()
+    assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
