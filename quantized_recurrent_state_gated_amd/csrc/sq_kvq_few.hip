@@ -29,6 +29,11 @@ using namespace kvq;
 // 16 bytes of a value column are one load, and the probabilities go from the first product
 // to the second in the lane's own registers.  Codes come from HBM in 16-byte
 // pieces (the order of d inside a product is free as long as q has the same).
+//
+// 70 requests to 16,384 tokens, 32 query and 8 key-value heads, d = 128: 223 us for 1.2 GB
+// of codes and scales, 5.4 TB/s (a copy of 2 GiB reaches 5.0), and 7 us for the join.  Three
+// contexts to 30,001, 20 and 4 heads, d = 64, fp32 queries: 13 and 4 us.  One request of
+// 201 tokens: 7.1 us, its loads one behind the other.
 
 constexpr int kMaxChunk = 8192;  // tokens per split at most (page ids kept in shared memory)
 constexpr int kPageIds = kMaxChunk / 16 + 4;
