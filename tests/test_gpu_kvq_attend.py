@@ -416,3 +416,21 @@ def test_larger_tiles_of_queries_that_are_not_finite(sq, new, ctx, H, Hkv):
     o2, lse2 = run(sq, c, q, t, lens, new, most=4400)
     assert torch.isnan(o2[hit]).all() and torch.isnan(lse2[hit]).all()
     assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+
+
+def test_prompts_of_pages_past_32_bits(sq):
+    """The same bits from pages whose bytes begin past 2^32, in both forms and tile sizes."""
+    lens, new, P, Hkv, d = [4500, 70], [40, 33], 256, 2, 128
+    c, t = ref.filled(lens, P, Hkv, d, "int8", 23)
+    dev = c.gpu(sq)
+    pages = 2 ** 32 // (P * Hkv * d) + c.pages
+    big = sq.SqKvqCache(*(torch.zeros(pages, *x.shape[1:], dtype=x.dtype, device="cuda")
+                          for x in (dev.k, dev.v, dev.scales)))
+    for a, b in ((big.k, dev.k), (big.v, dev.v), (big.scales, dev.scales)):
+        a[pages - c.pages:] = b
+    for dtype in ("bf16", "f32"):
+        q = queries(23, sum(new), 8, d, dtype)
+        for n, m in ((new, q), ([1, 1], q[:2])):
+            o, lse = run(sq, dev, m, t, lens, n)
+            o2, lse2 = run(sq, big, m, t + (pages - c.pages), lens, n)
+            assert torch.equal(o, o2) and torch.equal(lse, lse2) and o.abs().max() > 0
