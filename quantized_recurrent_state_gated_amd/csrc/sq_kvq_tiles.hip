@@ -269,15 +269,16 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
         }
         __builtin_amdgcn_sched_group_barrier(0x8, PARTS * 4, 0);
     };
-    // p and the sum of it from x, by the maximum so far
-    auto weigh = [&](const f32x4 (&sc)[4], const float (&fk)[4]) {
+    // p and the sum of it from x, by the maximum so far.  Where all value scales are within 2^-60 of their
+    // reference (`fold`), one float16 takes 2^(score - m) times the value scale in one exponential, and
+    // the sum takes the scale out again; smaller ones would take probabilities out of the sum.
+    auto weigh = [&](const f32x4 (&sc)[4], const float (&fk)[4], bool fold) {
         const float mu = m == -kInf ? 0.0f : m, c1 = up_log - mu;
         float sum = 0.0f;
 #pragma unroll
         for (int b = 0; b < 4; b++) {
             f32x8 t;
-            if constexpr (PARTS == 1) {
-                // 2^(score - mu) times the value scale in one exponential; the sum takes it out again
+            if (PARTS == 1 && fold) {
                 const float c0 = sc[2][b] + c1;
 #pragma unroll
                 for (int e = 0; e < 8; e++) t[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b >> 1][8 * (b & 1) + e], fk[b], c0));
@@ -290,7 +291,7 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
             }
             split8<PARTS>(t, p[b]);
         }
-        return PARTS == 1 ? sum * down : sum;
+        return PARTS == 1 && fold ? sum * down : sum;
     };
     auto weights = [&](int ring, int32_t base, uint32_t gone) {
         const f32x4 sc[4] = {sm_s[ring][0], sm_s[ring][1], sm_s[ring][2], sm_s[ring][3]};
@@ -313,13 +314,14 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
                 }
             }
         }
-        float sum = weigh(sc, fk);
+        float sum = weigh(sc, fk, true);
         // A tile whose weights pass 2^kGrow (their sum says so at the latest), the first of a
-        // row, or value scales past their reference: the maximum is found and the weights
-        // are made again.  Few tiles do.
+        // row, or value scales past their reference or far below it: the maximum is found and the
+        // weights are made again.  Few tiles do.
+        const float least = PARTS == 1 ? fminf(fminf(sc[1][0], sc[1][1]), fminf(sc[1][2], sc[1][3])) : kInf;
         const float most = fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3]));
         const bool grown = !(sum <= kGrown) || m == -kInf;
-        if (__ballot(grown || most > 2.0f * vref)) {
+        if (__ballot(grown || most > 2.0f * vref || least < 0x1p-60f * vref)) {
             float mx = in ? -kFloatMax : -kInf;
 #pragma unroll
             for (int b = 0; b < 4; b++)
@@ -337,7 +339,7 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
             up = kProbUp / v2, down = v2 * kProbDown, up_log = __builtin_log2f(up);
 #pragma unroll
             for (int i = 0; i < ND; i++) acc[i] *= fv;
-            sum = weigh(sc, fk);
+            sum = weigh(sc, fk, least >= 0x1p-60f * vref);
         }
         l += sum;
     };

@@ -1,0 +1,78 @@
+"""sq_kvq_attention where weights, value scales and scores lie far apart."""
+import numpy as np
+import pytest
+import torch
+
+import kvq_reference as ref
+import kvq_weights as kw
+from test_gpu_kvq_attend import FMT, ints, queries, run, sq  # noqa: F401 (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+# Requests (new tokens, tokens before), heads, key-value heads, width, bound of the lengths: one query a request,
+# a few, tiles of 128 rows and tiles of 256.
+FORMS = {"token": (None, [0, 15, 16, 70, 149], 4, 1, 64, 0), "few": ([4] * 5, [0, 14, 29, 60, 130], 4, 1, 64, 0),
+         "tiles": ([150, 33, 70, 0], [0, 31, 90, 20], 4, 1, 64, 0), "tiles256": ([40, 0, 64, 56], [0, 5, 70, 44], 4, 1, 128, 4400),
+         "splits": ([33, 40], [2100, 1500], 4, 1, 64, 0)}
+
+
+def shape(form):
+    new, ctx, H, Hkv, d, most = FORMS[form]
+    lens = [a + b for a, b in zip(ctx, new or [1] * len(ctx))]
+    cu = [0] + np.cumsum(new or [1] * len(ctx)).tolist()
+    return new, ctx, lens, cu, H, Hkv, d, most or max(lens)
+
+
+def held_scales(c, table, lens, which, of):
+    """Scales `of(block of its request)` for keys (0) or values (1)."""
+    for r, n in enumerate(lens):
+        for i in range(-(-n // 16)):
+            c.scales[table[r, 16 * i // c.P], :, 16 * i % c.P // 16, which] = of(i)
+
+
+def reaches(table, P, most):
+    """The table with room for `most` positions: pages that do not exist."""
+    more = max(0, -(-most // P) - table.shape[1])
+    return np.concatenate([table, np.full((table.shape[0], more), -1, table.dtype)], 1)
+
+
+def compare(o, lse, w, lim):
+    assert torch.isfinite(o).all()
+    off = (o - w[0]).abs()
+    assert (off <= lim[0]).all(), float((off / lim[0].clamp(min=1e-300)).max())
+    off = (lse - w[1]).abs()
+    assert (off <= lim[1]).all(), float((off / lim[1]).max())
+
+
+def check(sq, c, q, table, form, dtype, window=0):
+    new, _, lens, cu, _, _, d, most = shape(form)
+    o, lse = run(sq, c, q, reaches(table, c.P, most), lens, new, window=window, most=most)
+    w = ref.attention(c, q, table, lens, cu, d ** -0.5, window)
+    compare(o, lse, w, kw.limits(w, kw.floors(c, q, table, lens, cu, d ** -0.5, window), dtype))
+
+
+# ---------------------------------------------------------------- blocks of zeros
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_blocks_of_zeros_beside_large_values(sq, fmt, dtype, form):
+    """Padding and the like: blocks whose values are all zero, written by sq_kvq_append, before, after and among
+    blocks of large ones.  Their tokens count in the softmax as all others."""
+    new, ctx, lens, cu, H, Hkv, d, _ = shape(form)
+    g = torch.Generator().manual_seed(3)
+    table, pages = ref.tables(lens, 16, g)
+    at = [0] + np.cumsum(lens).tolist()
+    block = torch.cat([torch.arange(n) // 16 for n in lens])
+    q = queries(4, cu[-1], H, d, dtype)
+    for large, zero in ((1e3, (0, 2, 3, 7)), (1e9, (1, 2, 3, 8)), (1e13, (0, 1, 3, 4, 5)), (1e30, (0, 4, 5, 6, 7)),
+                        (1e30, (1, 3, 5, 7, 9))):
+        k = 0.1 * torch.randn(at[-1], Hkv, d, generator=g)
+        v = large * torch.randn(at[-1], Hkv, d, generator=g)
+        v[torch.isin(block, torch.tensor(zero))] = 0.0
+        c = ref.Cache(pages, Hkv, 16, d, fmt)
+        dev = c.gpu(sq)
+        sq.sq_kvq_append(dev, k.cuda(), v.cuda(), ints([0] * len(lens)), ints(at), torch.from_numpy(table).cuda())
+        c.append(k, v, [0] * len(lens), at, table)
+        c.same(dev)
+        check(sq, c, q, table, form, dtype)
