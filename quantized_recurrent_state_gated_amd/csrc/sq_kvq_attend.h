@@ -16,7 +16,9 @@
 //     two near the largest one seen (kept like the running maximum: when it grows,
 //     the sums so far are scaled down), and rounded to one float16 (11 bits, three
 //     more than the bfloat16 output; fp32 outputs take two).
-// Scores, maxima, sums of probabilities and outputs are fp32.
+// Scores, maxima, sums of probabilities and outputs are fp32.  Differences to the maximum
+// are taken of the products that it was found among, rounded as they were there:
+// past 2^24 a fused product and sum can lie a power of two and more above it.
 //
 // A row's maximum starts at -inf and is at least the lowest float once a key
 // is seen, so it says by itself whether any was: a row without keys has -inf
@@ -53,6 +55,13 @@ constexpr float kLn2 = 0.69314718055994531f;
 // float16's top, and its last place is 2^-29 of a probability of one
 constexpr float kProbUp = 32.0f, kProbDown = 1.0f / 32.0f;
 constexpr float kGrown = 256.0f;
+
+// a product that is not fused with what it is added to
+__device__ __forceinline__ float rounded(float a, float b)
+{
+#pragma clang fp contract(off)
+    return a * b;
+}
 
 template <bool E4M3>
 __device__ __forceinline__ h4 halves4(uint32_t w)

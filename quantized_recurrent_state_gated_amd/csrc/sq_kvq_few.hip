@@ -215,7 +215,7 @@ __global__ __launch_bounds__(256) void k_kvq_few(KvqAttendArgs a)
         float t[16];
 #pragma unroll
         for (int e = 0; e < 16; e++) {
-            t[e] = x[e / 4][e % 4] * fk;
+            t[e] = rounded(x[e / 4][e % 4], fk);
             if (edge && !(in >> e & 1)) t[e] = -kInf;
             mx = fmaxf(mx, t[e]);
         }

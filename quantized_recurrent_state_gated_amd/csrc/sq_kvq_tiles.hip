@@ -223,8 +223,9 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
         for (int e = 0; e < 16; e++) acc[i][e] = 0.0f;
     h8 p[4][PARTS];
     float m = -kInf, l = 0.0f;
-    float vref = 0x1p-111f;  // power of two under the value scales, and with it what p is kept times
-    float up = kProbUp / vref, down = vref * kProbDown, up_log = 116.0f;
+    // power of two under the value scales; what makes weights of probabilities, as a logarithm less m (where two
+    // float16 stand for a weight: as a factor); the least logarithm of a value scale that `weigh` is right for
+    float ref = 0x1p-111f, up = 0.0f, low = kInf;
 
     // element 8 (b % 2) + e of x[b / 2] is token 16 b + 8 hh + e of the tile
     const int krow = 16 * (c >> 4) + 8 * ((c >> 2) & 1) + 4 * ((c >> 3) & 1) + (c & 3);  // token of product row c
@@ -269,29 +270,35 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
         }
         __builtin_amdgcn_sched_group_barrier(0x8, PARTS * 4, 0);
     };
-    // p and the sum of it from x, by the maximum so far.  Where all value scales are within 2^-60 of their
-    // reference (`fold`), one float16 takes 2^(score - m) times the value scale in one exponential, and
-    // the sum takes the scale out again; smaller ones would take probabilities out of the sum.
-    auto weigh = [&](const f32x4 (&sc)[4], const float (&fk)[4], bool fold) {
-        const float mu = m == -kInf ? 0.0f : m, c1 = up_log - mu;
-        float sum = 0.0f;
+    // keeps a factor from the products made with it so far, which the compiler would hold on to for a
+    // second pass over the scores, in registers that it has not got
+    auto apart = [](float &f) { asm volatile("" : "+v"(f)); };
+    // Weights p of a tile and the sum of its probabilities, by maximum and reference as they
+    // stand; whether they could stand.
+    auto weigh = [&](const f32x4 (&sc)[4], const float (&fk)[4], float &sum) {
+        float least = PARTS == 1 ? sc[2][0] : 0.0f;
+        sum = 0.0f;
 #pragma unroll
         for (int b = 0; b < 4; b++) {
+            // One float16: 2^(score - m) times the value scale over the reference in one exponential; the
+            // sum takes the scale out again.  A scale 2^-60 under the reference could lose
+            // probabilities so, and scores past 2^10 the exponent's last bits: `low` says so.
+            const float c0 = PARTS == 1 ? sc[2][b] + up : -m;
             f32x8 t;
-            if (PARTS == 1 && fold) {
-                const float c0 = sc[2][b] + c1;
 #pragma unroll
-                for (int e = 0; e < 8; e++) t[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b >> 1][8 * (b & 1) + e], fk[b], c0));
-                sum = __builtin_fmaf(((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7])), sc[3][b], sum);
+            for (int e = 0; e < 8; e++) t[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b >> 1][8 * (b & 1) + e], fk[b], c0));
+            const float s8 = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+            if constexpr (PARTS == 1) {
+                sum = __builtin_fmaf(s8, sc[3][b], sum);
+                least = fminf(least, sc[2][b]);
             } else {
-#pragma unroll
-                for (int e = 0; e < 8; e++) t[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b >> 1][8 * (b & 1) + e], fk[b], -mu));
-                sum += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+                sum += s8;
                 t *= sc[1][b] * up;
             }
             split8<PARTS>(t, p[b]);
         }
-        return PARTS == 1 && fold ? sum * down : sum;
+        if constexpr (PARTS == 1) sum *= ref * kProbDown;
+        return sum <= kGrown && least >= low;
     };
     auto weights = [&](int ring, int32_t base, uint32_t gone) {
         const f32x4 sc[4] = {sm_s[ring][0], sm_s[ring][1], sm_s[ring][2], sm_s[ring][3]};
@@ -314,32 +321,70 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
                 }
             }
         }
-        float sum = weigh(sc, fk, true);
-        // A tile whose weights pass 2^kGrow (their sum says so at the latest), the first of a
-        // row, or value scales past their reference or far below it: the maximum is found and the
-        // weights are made again.  Few tiles do.
-        const float least = PARTS == 1 ? fminf(fminf(sc[1][0], sc[1][1]), fminf(sc[1][2], sc[1][3])) : kInf;
+        float sum;
+        const bool grown = !weigh(sc, fk, sum);
+        // Probabilities that pass 2^kGrown (their sum says so at the latest), the first tile of a row,
+        // scores past 2^10, value scales past their reference or far below it: the maximum is found
+        // and the weights are made again, probabilities first.  Few tiles do.
         const float most = fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3]));
-        const bool grown = !(sum <= kGrown) || m == -kInf;
-        if (__ballot(grown || most > 2.0f * vref || least < 0x1p-60f * vref)) {
+        if (__ballot(grown || most > 2.0f * ref)) {
+            // of the rows that need it alone: what another one holds must not show in a row's bits
+            const int other = __shfl_xor((int)grown, 32);
+            const bool need = grown || other || most > 2.0f * ref;
             float mx = in ? -kFloatMax : -kInf;
 #pragma unroll
-            for (int b = 0; b < 4; b++)
+            for (int b = 0; b < 4; b++) {
+                apart(fk[b]);
 #pragma unroll
-                for (int e = 0; e < 8; e++) mx = fmaxf(mx, x[b >> 1][8 * (b & 1) + e] * fk[b]);
-            // of the rows that need it alone: what another one holds (a NaN) must not show in a row
-            const int other_grown = __shfl_xor((int)grown, 32);
+                for (int e = 0; e < 8; e++) mx = fmaxf(mx, rounded(x[b >> 1][8 * (b & 1) + e], fk[b]));
+            }
             mx = fmaxf(mx, __shfl_xor(mx, 32));
-            const float mn = grown || other_grown ? fmaxf(m, mx) : m;
-            const float f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-            const float v2 = fmaxf(vref, bits_f(f_bits(most) & 0x7f800000u)), fv = f * (vref / v2);
-            m = mn;
-            l *= f;
-            vref = v2;
-            up = kProbUp / v2, down = v2 * kProbDown, up_log = __builtin_log2f(up);
+            const float mn = fmaxf(m, mx), mu = mn == -kInf ? 0.0f : mn;
+            const float r2 = fmaxf(ref, bits_f(f_bits(most) & 0x7f800000u));
+            float fv = ref / r2;
+            ref = r2;
+            if (need) {
+                const float f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+                m = mn;
+                l *= f;
+                fv *= f;
+            }
+            up = kProbUp / r2;
+            const bool near = __builtin_fabsf(m) <= 1024.0f;
+            if constexpr (PARTS == 1) {
+                const float up_log = __builtin_log2f(up);
+                low = near ? -55.0f - up_log : kInf;
+                up = up_log - m;
+            } else {
+                low = near ? 0.0f : kInf;
+            }
 #pragma unroll
             for (int i = 0; i < ND; i++) acc[i] *= fv;
-            sum = weigh(sc, fk, least >= 0x1p-60f * vref);
+            // what `weigh` makes of the other rows, and of these probabilities first, which are 1 at
+            // most: differences to the maximum are exact enough at any size of the scores
+            const float factor = kProbUp / ref;
+            sum = 0.0f;
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+                apart(fk[b]);
+                const float c0 = PARTS == 1 ? sc[2][b] + up : -m;
+                f32x8 t;
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const float s1 = x[b >> 1][8 * (b & 1) + e];
+                    t[e] = __builtin_amdgcn_exp2f(need ? rounded(s1, fk[b]) - mu : __builtin_fmaf(s1, fk[b], c0));
+                }
+                const float s8 = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+                if constexpr (PARTS == 1) {
+                    sum = __builtin_fmaf(s8, need ? 1.0f : sc[3][b], sum);
+                    t *= need ? sc[1][b] * factor : 1.0f;
+                } else {
+                    sum += s8;
+                    t *= sc[1][b] * up;
+                }
+                split8<PARTS>(t, p[b]);
+            }
+            if (PARTS == 1 && !need) sum *= ref * kProbDown;
         }
         l += sum;
     };
@@ -415,7 +460,7 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
     l += __shfl_xor(l, 32);
     if (!row_in) return;
     if (s.splits <= 1) {
-        const float inv = inverse_sum(m, l) * down;
+        const float inv = inverse_sum(m, l) * (ref * kProbDown);
         T *dst = reinterpret_cast<T *>(a.o) + out * D + 4 * hh;
 #pragma unroll
         for (int i = 0; i < ND; i++)
@@ -431,7 +476,7 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
         for (int i = 0; i < ND; i++)
 #pragma unroll
             for (int j = 0; j < 4; j++)
-                store4(dst + 32 * i + 8 * j, f32x4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]} * down);
+                store4(dst + 32 * i + 8 * j, f32x4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]} * (ref * kProbDown));
         if (hh == 0) {
             float *ml = part_o + (int64_t)a.n_q * a.q_heads * a.t_splits * D + at * 2;
             ml[0] = m;

@@ -76,3 +76,38 @@ def test_blocks_of_zeros_beside_large_values(sq, fmt, dtype, form):
         c.append(k, v, [0] * len(lens), at, table)
         c.same(dev)
         check(sq, c, q, table, form, dtype)
+
+
+# ---------------------------------------------------------------- scores of any size
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("power", [10, 17, 25, 28, 99])
+def test_large_scores_that_are_equal(sq, fmt, dtype, form, power):
+    """Equal keys have equal weights, whatever the scores are; where some keys' scores are larger, those have."""
+    new, _, lens, cu, H, Hkv, d, most = shape(form)
+    c, table = ref.filled(lens, 16, Hkv, d, fmt, power)
+    key = torch.randint(1, 100, (d,), generator=torch.Generator().manual_seed(1))
+    sharp = ref.Cache.__new__(ref.Cache)
+    sharp.__dict__.update(c.__dict__)
+    c.k[:] = (128 + key if fmt == "int8" else key.float().to(torch.float8_e4m3fn).view(torch.uint8)).to(torch.uint8)
+    sharp.k = c.k.clone()
+    one = 128 + 120 if fmt == "int8" else 0x70  # 128 as e4m3
+    for r, n in enumerate(lens):
+        for x in range(0, n, 37):
+            sharp.k[table[r, x // 16], :, x % 16] = one
+    held_scales(c, table, lens, 0, lambda i: 0.01)
+    for cc, q in ((c, queries(2, cu[-1], H, d, dtype)), (sharp, queries(2, cu[-1], H, d, dtype).abs() + 0.5)):
+        scale = 2.0 ** power / 64
+        o, lse = run(sq, cc, q, reaches(table, 16, most), lens, new, scale=scale, most=most)
+        # Weights are equal, or zero (some 100 nats below the others and more, all scores of one key are one
+        # number): 64 bits have them at a smaller scale, and what scores are rounded by does not enter o.
+        small = 0.0 if cc is c else min(scale, 2.0 ** 10 / 64)
+        floor = kw.floors(cc, q, table, lens, cu, small)
+        w = list(ref.attention(cc, q, table, lens, cu, small, 0))
+        w[3] = torch.zeros_like(w[3])
+        lim_o, _ = kw.limits(w, floor, dtype)
+        w[1], _, size = ref.attention(cc, q, table, lens, cu, scale, 0)[1:4]
+        w[3] = size
+        compare(o, lse, w, (lim_o, kw.limits(w, floor, dtype)[1]))
