@@ -12,10 +12,11 @@
 //     at 2^14 (bfloat16 queries are then exact down to 2^-31 of it, fp32 ones
 //     are two float16, 22 bits);
 //   - a score is (q.code) times its block's key scale, query scale and `scale`;
-//   - a probability is multiplied by its block's value scale over a power of
-//     two near the largest one seen (kept like the running maximum: when it grows,
-//     the sums so far are scaled down), and rounded to one float16 (11 bits, three
-//     more than the bfloat16 output; fp32 outputs take two).
+//   - a probability is multiplied by its block's value scale over the largest such
+//     product that its row has seen (kept like the running maximum: when it grows, the sums
+//     so far are scaled down), and rounded to one float16 (11 bits, three more than
+//     the bfloat16 output; fp32 outputs take two).  That reference is the row's own: tokens
+//     that it does not see, or whose weight is small, do not move it.
 // Scores, maxima, sums of probabilities and outputs are fp32.  Differences to the maximum
 // are taken of the products that it was found among, rounded as they were there:
 // past 2^24 a fused product and sum can lie a power of two and more above it.
@@ -50,11 +51,15 @@ constexpr float kInf = __builtin_inff();
 constexpr float kFloatMax = 3.402823466e+38f;
 constexpr float kTiny = 1.17549435e-38f;
 constexpr float kLn2 = 0.69314718055994531f;
-// probabilities are kept as float16 times 32: the largest, 2^8 (the tile form lets a
-// row's maximum stand until weights pass 2^8) x 2 (value scale) x 32, stays below
-// float16's top, and its last place is 2^-29 of a probability of one
+// Weights (probabilities times value scales over the reference) are kept as float16 times 32:
+// its last place is 2^-29 of a weight of one.  The tile form lets maximum and reference stand
+// until a lane's probabilities of a tile pass 2^8, or its weights float16's top.
 constexpr float kProbUp = 32.0f, kProbDown = 1.0f / 32.0f;
-constexpr float kGrown = 256.0f;
+constexpr float kGrown = 256.0f, kMostWeight = 32768.0f;
+// Probabilities of 2^-120 and less may lose their bits, or count as zero: they do not enter the reference,
+// and the factor that makes weights of them ends at 2^126.  References end at 2^-111,
+// under the smallest scale.
+constexpr float kLeastProb = -120.0f, kMostFactor = 0x1p126f, kLeastRef = 0x1p-111f;
 
 // a product that is not fused with what it is added to
 __device__ __forceinline__ float rounded(float a, float b)
@@ -62,6 +67,14 @@ __device__ __forceinline__ float rounded(float a, float b)
 #pragma clang fp contract(off)
     return a * b;
 }
+// weight (before it is divided by the reference) of a block's largest score
+__device__ __forceinline__ float top_weight(float score, float m, float scale)
+{
+    const float d = score - m;
+    return d >= kLeastProb ? __builtin_amdgcn_exp2f(d) * scale : 0.0f;
+}
+// what turns a block's probabilities into weights
+__device__ __forceinline__ float factor_of(float scale, float up) { return fminf(scale * up, kMostFactor); }
 
 template <bool E4M3>
 __device__ __forceinline__ h4 halves4(uint32_t w)

@@ -146,7 +146,7 @@ __global__ __launch_bounds__(256) void k_kvq_few(KvqAttendArgs a)
 #pragma unroll
     for (int i = 0; i < ND; i++) acc[i] = f32x4{0, 0, 0, 0};
     float m = -kInf, l = 0.0f;
-    float vref = 0x1p-111f;  // power of two under the value scales: at most twice it
+    float ref = 0.0f;  // the row's largest weight, times 2^m
 
     u32x4_t kf[4][NW > 0 ? NW : 1];
     u32x2_t kt[4];
@@ -211,32 +211,33 @@ __global__ __launch_bounds__(256) void k_kvq_few(KvqAttendArgs a)
             }
         }
         const float fk = fmaxf(sk * qscale, kTiny);
-        float mx = in ? -kFloatMax : -kInf;
+        float mb = -kInf;  // of the block
         float t[16];
 #pragma unroll
         for (int e = 0; e < 16; e++) {
             t[e] = rounded(x[e / 4][e % 4], fk);
             if (edge && !(in >> e & 1)) t[e] = -kInf;
-            mx = fmaxf(mx, t[e]);
+            mb = fmaxf(mb, t[e]);
         }
+        float mx = fmaxf(in ? -kFloatMax : -kInf, mb);
         mx = fmaxf(mx, __shfl_xor(mx, 16));
         mx = fmaxf(mx, __shfl_xor(mx, 32));
-        if (__ballot(mx > m || sv > 2.0f * vref)) {
-            float most = sv;
-            most = fmaxf(most, __shfl_xor(most, 16));
-            most = fmaxf(most, __shfl_xor(most, 32));
-            const float v2 = fmaxf(vref, bits_f(f_bits(most) & 0x7f800000u));
+        if (__ballot(mx > m || top_weight(mb, m, sv) > ref)) {  // rows that need neither keep their bits
             const float mn = fmaxf(m, mx);
             const float f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             m = mn;
             l *= f;
-            const float fv = f * (vref / v2);
-            vref = v2;
+            float top = top_weight(mb, mn, sv);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float r2 = fmaxf(fmaxf(ref * f, top), kLeastRef);
+            const float fv = f * (ref / r2);
+            ref = r2;
 #pragma unroll
             for (int i = 0; i < ND; i++) acc[i] *= fv;
         }
         const float mu = m == -kInf ? 0.0f : m;
-        const float wv_ = sv * (kProbUp / vref);
+        const float wv_ = factor_of(sv, kProbUp / ref);
 #pragma unroll
         for (int e = 0; e < 16; e++) {
             t[e] = __builtin_amdgcn_exp2f(t[e] - mu);
@@ -274,7 +275,7 @@ __global__ __launch_bounds__(256) void k_kvq_few(KvqAttendArgs a)
         const float mw = sm_m[w][c];
         L += mw == -kInf ? 0.0f : sm_l[w][c] * __builtin_amdgcn_exp2f(mw - M);
     }
-    const float f = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(m - M) * (vref * kProbDown);
+    const float f = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(m - M) * (ref * kProbDown);
 #pragma unroll
     for (int i = 0; i < ND; i++) acc[i] *= f;
     if (wv > 0) {

@@ -198,7 +198,7 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
     // scales by the first lanes of one wave, block by block: a lane's block of a tile
     const bool scaler = wv == WAVES - 1 && lane < 4;
     auto fetch_scales = [&](int32_t base, int32_t id) {
-        f32x2 sc = {1.0f, 0.0f};
+        f32x2 sc = {1.0f, 1.0f};
         // where no row sees a position of the block, what lies there need not be a scale
         if (scaler) {
             const int32_t x = base + 16 * lane;
@@ -223,9 +223,9 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
         for (int e = 0; e < 16; e++) acc[i][e] = 0.0f;
     h8 p[4][PARTS];
     float m = -kInf, l = 0.0f;
-    // power of two under the value scales; what makes weights of probabilities, as a logarithm less m (where two
-    // float16 stand for a weight: as a factor); the least logarithm of a value scale that `weigh` is right for
-    float ref = 0x1p-111f, up = 0.0f, low = kInf;
+    // the row's largest weight, times 2^m; what makes weights of probabilities, as a logarithm less m (where two float16
+    // stand for a weight: as a factor); the least logarithm of a value scale that `weigh` is right for
+    float ref = 0.0f, up = 0.0f, low = kInf;
 
     // element 8 (b % 2) + e of x[b / 2] is token 16 b + 8 hh + e of the tile
     const int krow = 16 * (c >> 4) + 8 * ((c >> 2) & 1) + 4 * ((c >> 3) & 1) + (c & 3);  // token of product row c
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
     // Weights p of a tile and the sum of its probabilities, by maximum and reference as they
     // stand; whether they could stand.
     auto weigh = [&](const f32x4 (&sc)[4], const float (&fk)[4], float &sum) {
-        float least = PARTS == 1 ? sc[2][0] : 0.0f;
+        float most = 0.0f, least = PARTS == 1 ? sc[2][0] : 0.0f;
         sum = 0.0f;
 #pragma unroll
         for (int b = 0; b < 4; b++) {
@@ -290,15 +290,18 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
             const float s8 = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
             if constexpr (PARTS == 1) {
                 sum = __builtin_fmaf(s8, sc[3][b], sum);
+                most += s8;
                 least = fminf(least, sc[2][b]);
             } else {
+                const float g = factor_of(sc[1][b], up);
                 sum += s8;
-                t *= sc[1][b] * up;
+                most = __builtin_fmaf(s8, g, most);
+                t *= g;
             }
             split8<PARTS>(t, p[b]);
         }
         if constexpr (PARTS == 1) sum *= ref * kProbDown;
-        return sum <= kGrown && least >= low;
+        return sum <= kGrown && most <= kMostWeight && least >= low;
     };
     auto weights = [&](int ring, int32_t base, uint32_t gone) {
         const f32x4 sc[4] = {sm_s[ring][0], sm_s[ring][1], sm_s[ring][2], sm_s[ring][3]};
@@ -323,40 +326,45 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
         }
         float sum;
         const bool grown = !weigh(sc, fk, sum);
-        // Probabilities that pass 2^kGrown (their sum says so at the latest), the first tile of a row,
-        // scores past 2^10, value scales past their reference or far below it: the maximum is found
-        // and the weights are made again, probabilities first.  Few tiles do.
-        const float most = fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3]));
-        if (__ballot(grown || most > 2.0f * ref)) {
+        // Probabilities that pass 2^kGrown or weights that pass float16 (their sums say so at
+        // the latest), the first tile of a row, scales or scores too far apart: maximum and
+        // reference are found and the weights made again, probabilities first.  Few tiles do.
+        if (__ballot(grown)) {
             // of the rows that need it alone: what another one holds must not show in a row's bits
             const int other = __shfl_xor((int)grown, 32);
-            const bool need = grown || other || most > 2.0f * ref;
-            float mx = in ? -kFloatMax : -kInf;
+            const bool need = grown || other;
+            float mb[4], mx = in ? -kFloatMax : -kInf;
 #pragma unroll
             for (int b = 0; b < 4; b++) {
                 apart(fk[b]);
+                mb[b] = -kInf;
 #pragma unroll
-                for (int e = 0; e < 8; e++) mx = fmaxf(mx, rounded(x[b >> 1][8 * (b & 1) + e], fk[b]));
+                for (int e = 0; e < 8; e++) mb[b] = fmaxf(mb[b], rounded(x[b >> 1][8 * (b & 1) + e], fk[b]));
+                mx = fmaxf(mx, mb[b]);
             }
             mx = fmaxf(mx, __shfl_xor(mx, 32));
             const float mn = fmaxf(m, mx), mu = mn == -kInf ? 0.0f : mn;
-            const float r2 = fmaxf(ref, bits_f(f_bits(most) & 0x7f800000u));
-            float fv = ref / r2;
-            ref = r2;
+            float top = 0.0f;
+#pragma unroll
+            for (int b = 0; b < 4; b++) top = fmaxf(top, top_weight(mb[b], mu, sc[1][b]));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            float fv = 1.0f;
             if (need) {
                 const float f = mn == -kInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+                const float r2 = fmaxf(fmaxf(ref * f, top), kLeastRef);
+                fv = f * (ref / r2);
                 m = mn;
                 l *= f;
-                fv *= f;
-            }
-            up = kProbUp / r2;
-            const bool near = __builtin_fabsf(m) <= 1024.0f;
-            if constexpr (PARTS == 1) {
-                const float up_log = __builtin_log2f(up);
-                low = near ? -55.0f - up_log : kInf;
-                up = up_log - m;
-            } else {
-                low = near ? 0.0f : kInf;
+                ref = r2;
+                up = kProbUp / r2;
+                const bool near = __builtin_fabsf(m) <= 1024.0f;
+                if constexpr (PARTS == 1) {
+                    const float up_log = __builtin_log2f(up);
+                    low = near ? -55.0f - up_log : kInf;
+                    up = up_log - m;
+                } else {
+                    low = near ? 0.0f : kInf;
+                }
             }
 #pragma unroll
             for (int i = 0; i < ND; i++) acc[i] *= fv;
@@ -377,10 +385,10 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
                 const float s8 = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
                 if constexpr (PARTS == 1) {
                     sum = __builtin_fmaf(s8, need ? 1.0f : sc[3][b], sum);
-                    t *= need ? sc[1][b] * factor : 1.0f;
+                    t *= need ? factor_of(sc[1][b], factor) : 1.0f;
                 } else {
                     sum += s8;
-                    t *= sc[1][b] * up;
+                    t *= factor_of(sc[1][b], up);
                 }
                 split8<PARTS>(t, p[b]);
             }

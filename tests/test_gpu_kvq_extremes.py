@@ -111,3 +111,37 @@ def test_large_scores_that_are_equal(sq, fmt, dtype, form, power):
         w[1], _, size = ref.attention(cc, q, table, lens, cu, scale, 0)[1:4]
         w[3] = size
         compare(o, lse, w, (lim_o, kw.limits(w, floor, dtype)[1]))
+
+
+# ---------------------------------------------------------------- value scales of tokens that a row does not see
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("step,window", [(3, 0), (10, 0), (20, 0), (-10, 20), (-20, 40)])
+def test_value_scales_of_tokens_not_seen(sq, fmt, dtype, form, step, window):
+    """Value scales that rise from block to block, by 2^3 to 2^20 (four blocks, then from the start), and fall in
+    front of a window: a row's weights have their bits beside what later rows see."""
+    new, _, lens, cu, H, Hkv, d, _ = shape(form)
+    c, table = ref.filled(lens, 16, Hkv, d, fmt, 31)
+    held_scales(c, table, lens, 0, lambda i: 1 / 64)
+    held_scales(c, table, lens, 1, lambda i: 1.3 * 2.0 ** (step * (i % 4) - 2))
+    check(sq, c, queries(5, cu[-1], H, d, dtype), table, form, dtype, window)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_large_values_of_small_weight(sq, fmt, dtype, form):
+    """Tokens of value scales 2^40 and weights near 2^-60 beside others of 2^-20 and 1."""
+    new, _, lens, cu, H, Hkv, d, _ = shape(form)
+    c, table = ref.filled(lens, 16, Hkv, d, fmt, 33)
+    held_scales(c, table, lens, 1, lambda i: 2.0 ** 40 if i % 3 == 1 else 0.7 * 2.0 ** -20)
+    # keys of one code: + in most blocks, - where values are large; queries of one sign
+    for r, n in enumerate(lens):
+        for x in range(n):
+            far = x // 16 % 3 == 1
+            c.k[table[r, x // 16], :, x % 16] = (128 - 64 if far else 128 + 64) if fmt == "int8" else (0xe8 if far else 0x68)
+    held_scales(c, table, lens, 0, lambda i: 1 / 64)
+    q = (1 + 0.01 * queries(5, cu[-1], H, d, dtype).float().abs()) * (20.6 / d ** 0.5)  # scores of +-20.6: e^41 is 2^60
+    check(sq, c, q.to(ref.DT[dtype]), table, form, dtype)
