@@ -445,7 +445,8 @@ typedef struct {
  *         aligned, tokens k_stride / v_stride elements apart (a multiple of 16
  *         bytes).
  * Tokens of pages outside the cache or past the table's row are skipped, and so
- * are requests with a negative length; cu_new is held to [0, n_tok].  A page
+ * are requests with a negative length; cu_new is held to [0, n_tok] and must not fall
+ * (some tokens are left out then, and nothing else is touched).  A page
  * that gets tokens must belong to one request of the batch.  n_tok == 0 or n_req
  * == 0 is a no-op.  `cache` is a HOST struct, read during the call.
  * Errors: SQ_ERR_INVALID (null or misaligned pointer, bad size, stride or enum),
@@ -474,7 +475,8 @@ uint64_t sq_kvq_attention_workspace(const sq_kvq_cache *cache, int32_t n_req, in
 
 /* Attention over the 8-bit cache, of one new token per request (cu_q NULL, n_q
  * == n_req) or of the last cu_q[r + 1] - cu_q[r] tokens of each (cu_q DEVICE int32
- * [n_req + 1], held to [0, n_q]): prompts, pieces of prompts, single tokens, mixed.
+ * [n_req + 1], held to [0, n_q] and not falling, as cu_new above): prompts, pieces of
+ * prompts, single tokens, mixed.
  * The tokens' own keys and values are appended before.  Query i of m of a request
  * of L = seq_lens[r] tokens stands at position L - m + i and
  *     o = sum_x p_x v_x,  p = softmax over x of scale q . k_x

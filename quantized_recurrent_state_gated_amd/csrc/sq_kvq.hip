@@ -253,9 +253,10 @@ __device__ __forceinline__ Place place_of(const KvqRowsArgs &a, int64_t slot)
     const int r = request_of(a, slot, t0, t1, start);
     Place p{0, 0, r, 0, 0};
     if (r < 0) return p;
-    if (start < 0 || t1 <= t0) return p;
+    const int64_t nth = slot - ((t0 >> 4) + 2 * (int64_t)r);  // of the request's slots; negative where offsets fall
+    if (start < 0 || t1 <= t0 || nth < 0) return p;
     const int64_t end = (int64_t)start + (t1 - t0);
-    const int64_t b = (start >> 4) + slot - ((t0 >> 4) + 2 * (int64_t)r);  // block of the request
+    const int64_t b = (start >> 4) + nth;  // block of the request
     const int64_t pos = b << 4;
     if (pos >= end) return p;
     p.tok = t0 + pos - start;

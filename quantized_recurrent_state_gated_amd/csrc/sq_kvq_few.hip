@@ -420,7 +420,7 @@ __device__ __forceinline__ void join_tiles(const KvqAttendArgs &a, int64_t out)
     const int r = wave_count(a.n, [&](int i) { return clamp_to(a.cu[i], a.n_q) <= qi; }) - 1;
     if (r < 0) return;
     const Req q = req_of(a, r);
-    if (qi >= q.q0 + q.m || few(a, q.m)) return;
+    if (qi < q.q0 || qi >= q.q0 + q.m || few(a, q.m)) return;  // padding; offsets that fall
     // the row's tile, as the tiles were cut
     const int64_t rows = (int64_t)q.m * a.group;
     const int64_t tile = a.tile_rows;

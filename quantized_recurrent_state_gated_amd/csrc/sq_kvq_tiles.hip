@@ -83,6 +83,7 @@ __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) vo
         r = wave_count(a.n, [&](int i) { return (int64_t)clamp_to(a.cu[i], a.n_q) * a.group / ROWS + i <= back; }) - 1;
         if (r < 0) return;
         tile = back - ((int64_t)clamp_to(a.cu[r], a.n_q) * a.group / ROWS + r);
+        if (tile < 0) return;  // where offsets fall
     }
     const Req q = req_of(a, r);
     if (q.m < 1 || few(a, q.m)) return;
