@@ -38,3 +38,14 @@ def limits(w, floor, dtype):
     p = {"bf16": 2.0 ** -11, "f32": 2.0 ** -21}[dtype]
     return ((near + p)[..., None] * mag + half * o.abs() + (2.0 ** -30 * floor[0] + 2.0 ** -120 * floor[1])[..., None],
             near + 2.0 ** -22 * torch.where(lse.isinf(), 0.0, lse.abs()))
+
+
+def exact_limits(w, floor, count):
+    """fp32 outputs of queries with a single value that is not zero.  A score is then one product: its query has
+    22 bits (2^-22), its two parts are added once (2^-23), the factors of the scales round four times (4 x 2^-24),
+    together under 2^-20.6; so is the maximum's, and the difference of both is off by under 2^-19 of the scores.  An
+    exponential adds 2^-22, the weight's two float16 2^-22 and its products 2^-23; sums round once a token and
+    part, the output's factors three times."""
+    o, _, mag, size, _ = w
+    p = 2.0 ** -19 * size + 2.0 ** -21 + 2.0 ** -23 + (2 * count + 3) * 2.0 ** -23
+    return p[..., None] * mag + 2.0 ** -24 * o.abs() + (2.0 ** -30 * floor[0] + 2.0 ** -120 * floor[1])[..., None]

@@ -145,3 +145,28 @@ def test_large_values_of_small_weight(sq, fmt, dtype, form):
     held_scales(c, table, lens, 0, lambda i: 1 / 64)
     q = (1 + 0.01 * queries(5, cu[-1], H, d, dtype).float().abs()) * (20.6 / d ** 0.5)  # scores of +-20.6: e^41 is 2^60
     check(sq, c, q.to(ref.DT[dtype]), table, form, dtype)
+
+
+# ---------------------------------------------------------------- the bits of fp32 calls
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("form", ["token", "few", "tiles"])
+@pytest.mark.parametrize("d", [32, 128])
+@pytest.mark.parametrize("size", [0.5, 16.0])
+def test_full_precision_of_f32(sq, fmt, form, d, size):
+    """Few tokens, and queries of one value that is not zero: 22 bits of query and weight are all there."""
+    new = {"token": None, "few": [3, 2, 3, 1], "tiles": [5, 5, 3, 6]}[form]
+    lens = {"token": [2, 3, 5, 2, 3], "few": [3, 3, 5, 2], "tiles": [5, 6, 3, 7]}[form]
+    cu = [0] + np.cumsum(new or [1] * len(lens)).tolist()
+    H = 16 if form == "tiles" else 4
+    c, table = ref.filled(lens, 16, 1, d, fmt, d)
+    g = torch.Generator().manual_seed(d)
+    q = torch.zeros(cu[-1], H, d)
+    at = torch.randint(0, d, (cu[-1], H, 1), generator=g)
+    top = 64 * (127 if fmt == "int8" else 120) ** -1.0
+    q.scatter_(2, at, size * top * (0.5 + 0.5 * torch.rand(cu[-1], H, 1, generator=g)))
+    o, _ = run(sq, c, q, table, lens, new, scale=1.0)
+    w = ref.attention(c, q, table, lens, cu, 1.0, 0)
+    lim = kw.exact_limits(w, kw.floors(c, q, table, lens, cu, 1.0), max(lens))
+    off = (o - w[0]).abs()
+    assert (off <= lim).all(), float((off / lim).max())
