@@ -495,8 +495,9 @@ uint64_t sq_kvq_attention_workspace(const sq_kvq_cache *cache, int32_t n_req, in
  * value scale, is kept to 11 bits (fp32 outputs: 22) and to 2^-30 of the largest
  * weight of its row; p_x under 2^-120 of the row's largest may count as zero.  What the cache
  * holds outside the positions that a request's queries see is not used, and what a query does
- * not see has no part in its row.  Values are summed before they are divided by the
- * softmax's sum: sums past the fp32 range are infinite.  n_req == 0 or n_q == 0 is a no-op.  Errors: SQ_ERR_INVALID (null or misaligned pointer, bad size, workspace
+ * not see has no part in its row.  Values may be summed before they are divided by the
+ * softmax's sum: sums past the fp32 range are infinite then.  n_req == 0 or n_q == 0 is a
+ * no-op.  Errors: SQ_ERR_INVALID (null or misaligned pointer, bad size, workspace
  * too small), SQ_ERR_UNSUPPORTED (page_size, head_dim, launch grid, more than 2^30
  * tokens or 2^30 - 1 rows of requests or queries x heads), SQ_ERR_HIP.
  * Asynchronous on `stream`; the workspace is in use until the call's work is done. */

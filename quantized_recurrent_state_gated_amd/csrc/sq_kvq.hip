@@ -480,7 +480,8 @@ __global__ __launch_bounds__(256) void k_kvq_append(KvqRowsArgs a, uint32_t wave
 
 // ---------------------------------------------------------------- read back
 //
-// Bound by HBM: 8 requests to 8,192 tokens x 8 heads, d = 128 into bfloat16, 37 us (231 MB).
+// Bound by HBM: 8 requests to 8,192 tokens x 8 heads, d = 128 into bfloat16 (231 MB): 55 us for a call on
+// a cache that it finds in HBM, 4.2 TB/s; 37 us of kernel where part of it lies in the last-level cache.
 
 template <typename T, int D, bool E4M3>
 __device__ __forceinline__ void load_keys(const KvqRowsArgs &a, const Place &p, int h)

@@ -32,8 +32,8 @@ using namespace kvq;
 //
 // 70 requests to 16,384 tokens, 32 query and 8 key-value heads, d = 128: 223 us for 1.2 GB
 // of codes and scales, 5.4 TB/s (a copy of 2 GiB reaches 5.0), and 7 us for the join.  Three
-// contexts to 30,001, 20 and 4 heads, d = 64, fp32 queries: 13 and 4 us.  One request of
-// 201 tokens: 7.1 us, its loads one behind the other.
+// contexts to 30,001, 20 and 4 heads, d = 64, fp32 queries: 14 and 4 us.  One request of
+// 201 tokens: 7.2 us, its loads one behind the other.
 
 constexpr int kMaxChunk = 8192;  // tokens per split at most (page ids kept in shared memory)
 constexpr int kPageIds = kMaxChunk / 16 + 4;
@@ -518,9 +518,10 @@ uint64_t kvq_plan(KvqAttendArgs &a, bool bf16)
     uint64_t bytes = 0;
 
     // The tile form takes any number of queries.  The other one is worth its launches where
-    // requests of few queries are likely (the mean says so) or have long contexts: a
-    // single token among prompts, over 500, 1,000 and 2,000 tokens (31 beside a prompt of
-    // 512, 8 heads of 4): 50, 72 and 111 us with it, 43, 67 and 114 without.
+    // requests of few queries are likely (the mean says so) or have long contexts: single
+    // tokens among prompts, 8 heads of 4: 31 beside a prompt of 512 over 500, 1,000, 2,000 and 8,000
+    // tokens 57, 78, 95 and 271 us with it, 42, 55, 102 and 295 without; 12 beside 4 of 200 42, 58, 90 and
+    // 202, and 30, 45, 76 and 270.
     a.few_on = !tiled || (a.n > 1 && (most > 2048 || (int64_t)a.n_q * a.group <= 16 * (int64_t)a.n));
     a.rows = (int32_t)rows_few(one, a.group);
     a.q_tiles = a.few_on ? (a.rows + 15) / 16 : 0;
@@ -569,15 +570,15 @@ uint64_t kvq_plan(KvqAttendArgs &a, bool bf16)
         // Tiles of 256 rows stage a token half as often, and their waves take turns; of 128
         // rows there are two workgroups a unit, each of which ends beside the other's work.
         // Measured (8 heads of 4, us with 256 and 128):
-        //   long contexts, many rounds of tiles: one prompt of 8,192 572 and 600
-        //   fewer rounds, the last one decides: one of 6,000 344 and 336, 8 x 512 behind 4,000
-        //   315 and 333, two sets of 6 ragged behind 6,000 274 and 260, 274 and 275
-        //   short ones: 20 x 800 236 and 212, 8,192 tokens in a window of 1,024 196 and 185
-        //   few rows, 256 hold them as well as 2 x 128: 33 behind 60,000 76 and 86, 30 x 40
-        //   behind 8,000 256 and 292; not so: 20 behind 60,000 69 and 52, 80 behind 30,000
-        //   82 and 72
+        //   long contexts, many rounds of tiles: one prompt of 8,192 595 and 614
+        //   fewer rounds, the last one decides: one of 6,000 350 and 341, 8 x 512 behind 4,000
+        //   325 and 333, 6 ragged behind 6,000 289 and 277
+        //   short ones: 20 x 800 239 and 217, 8,192 tokens in a window of 1,024 205 and 195
+        //   few rows, 256 hold them as well as 2 x 128: 33 behind 60,000 73 and 82, 30 x 40
+        //   behind 8,000 267 and 298; not so: 20 behind 60,000 70 and 54, 80 behind 30,000
+        //   81 and 74
         // and where d is not 128, or two float16 stand for a query, 128 everywhere (d = 64, one
-        // prompt of 8,192: 502 and 399, 20 x 800 195 and 151).
+        // prompt of 8,192: 504 and 420, 20 x 800 197 and 155).
         const int64_t mean = ((int64_t)a.n_q * a.group + a.n - 1) / a.n;
         const bool even = (mean + 255) / 256 * 256 <= (mean + 127) / 128 * 128;
         if (tiles_of_256(bf16, a.c.d) && most >= 4096 && even) cut(256);

@@ -24,14 +24,15 @@ using namespace kvq;
 // lane's 8 scores of a block are the second product's operand in its own registers.
 //
 // What bounds it: a wave's tile is 32 products of 32 cycles, and 32 exponentials of 16
-// cycles and some 170 other vector instructions a lane.  A product takes about 16 of its
+// cycles and some 180 other vector instructions a lane.  A product takes about 16 of its
 // cycles from the other wave's vector instructions on the SIMD (measured), so turns of
 // products beside turns of weights cannot do with less than about 1,800 cycles
 // for two waves' halves; they take 2,400.  One causal prompt of 8,192 tokens, 32 query and 8
-// key-value heads, d = 128 in integer codes: 572 to 587 us, 935 to 960 TFLOP/s (a
-// float16 library product of 8192^3 reaches 1,092).  On the way: 1,046 us with one wave a
-// SIMD, 660 with two that are not kept apart, 820 with turns but page ids waited for one by
-// one, 631 with the maximum looked for in every tile.
+// key-value heads, d = 128 in integer codes: 590 to 615 us, 895 to 930 TFLOP/s, with other
+// work or pauses between; 20 of them back to back 660 to 780, 704 on average, 780 TFLOP/s (a float16
+// library product of 8192^3, back to back, reaches 1,092).  On the way: 1,046 us with one
+// wave a SIMD, 660 with two that are not kept apart, 820 with turns but page ids waited for
+// one by one, 631 with the maximum looked for in every tile.
 
 template <typename T, bool E4M3, int D, int ROWS>
 __global__ __launch_bounds__(2 * ROWS, two_a_simd(sizeof(T) == 2, D) ? 2 : 1) void k_kvq_tiles(KvqAttendArgs a)
