@@ -413,6 +413,8 @@ int sq_paged_attention(const sq_kv_cache *cache, const void *q, int64_t q_stride
  *     SQ_KVQ_E4M3  c = the OCP e4m3 number u (no infinities, largest 448)
  * Scales written by sq_kvq_append are at least 2^-100; in a cache made elsewhere they
  * may be smaller, or zero, and attention may take value scales below that as 2^-100.
+ * Tokens' scales are finite and not negative and their codes numbers (no e4m3 NaN, 0x7f
+ * and 0xff): this is not checked, and a NaN may show in every row of a request.
  * Requests, pages and block tables are those of the paged cache above
  * (sq_block_tables).  Pages may hold anything past a request's last token,
  * scales included. */
